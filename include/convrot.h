@@ -81,7 +81,7 @@
 extern "C" {
 #endif
 
-#define CONVROT_ABI_VERSION 10
+#define CONVROT_ABI_VERSION 11
 
 typedef enum {
   CONVROT_OK = 0,
@@ -120,7 +120,8 @@ typedef enum {
 typedef enum {
   CONVROT_ACT_NONE = 0, /* not accepted by the fused entry points (use convrot_linear) */
   CONVROT_ACT_GELU_ERF = 1,
-  CONVROT_ACT_GELU_TANH = 2
+  CONVROT_ACT_GELU_TANH = 2,
+  CONVROT_ACT_SILU = 3 /* y / (1 + e^{-y}), hardware exp2 and reciprocal; the grouped linears only */
 } convrot_act;
 
 /* Which linear entry point a workspace query is for
@@ -539,6 +540,177 @@ convrot_status convrot_lora_add(const void* X, int64_t ldx, int64_t M, int64_t K
                                 const void* B, int64_t ldb, int64_t N, int64_t r, float scale, void* Y,
                                 convrot_dtype ydt, int64_t ldy, void* workspace, int64_t workspace_bytes,
                                 void* stream);
+
+/* ---------------------------------------------------------------------
+ * Rows that choose their weights
+ * ---------------------------------------------------------------------
+ * A batch's rows may go through different weights: tokens routed to experts,
+ * requests with adapters of their own.  Each row makes k choices ("pairs":
+ * pair p belongs to row p / k), a choice is an id in [0, groups), and any
+ * other id (-1) is a pair without a group.
+ *   convrot_route         router logits -> ids and weights
+ *   convrot_group_rows    ids -> plan: the pairs in the order of their groups
+ *   convrot_linear_grouped, convrot_linear_gated_grouped
+ *                         quantised linears over stacked weights
+ *   convrot_combine_rows  the weighted sum of every row's k outputs
+ *   convrot_lora_add_grouped
+ *                         adapters per row
+ * Group sizes stay on the device: no call waits for the GPU, and every call
+ * may be captured into a graph and replayed with new ids in place. */
+
+/* Scores of convrot_route. */
+typedef enum {
+  CONVROT_SCORE_SOFTMAX = 0, /* over the row's experts */
+  CONVROT_SCORE_SIGMOID = 1  /* per expert */
+} convrot_score;
+
+/* A router's rule. */
+typedef struct {
+  int32_t score;       /* convrot_score */
+  int32_t top_k;       /* k, at most 64 and at most the experts of the groups kept */
+  int32_t groups;      /* groups of consecutive experts, 1 to 64, a divisor of E */
+  int32_t top_groups;  /* groups kept, 1 to groups */
+  int32_t renormalise; /* nonzero: the k weights are divided by their sum */
+  float scale;         /* factor of every weight */
+} convrot_routing;
+
+/* The choice of experts.  For a row of E logits l:
+ *   s_i = e^{l_i} / sum_j e^{l_j}, or 1 / (1 + e^{-l_i})
+ *   c_i = s_i + bias_i      used for the choice only (a bias for balance)
+ *   the value of a group of experts is the sum of its two largest c (its
+ *   only one where it has one); the top_groups largest values are kept
+ *   ids[m, 0..k)  the k largest c among the kept groups' experts, in
+ *                 descending order
+ *   weights[m, j] = s[ids[m, j]] (over the k scores' sum if renormalised)
+ *                   * scale
+ * Ties go to the lowest index, in both choices.  A logit of -inf or NaN
+ * closes an expert: it counts nowhere and is not chosen.  A bias of -inf or
+ * NaN only keeps its expert from being chosen and from its group's value.  A
+ * group without such an expert left is not kept.  Where fewer than k
+ * experts are left, the remaining ids are -1 and their weights 0; a sum of
+ * zero leaves zero weights.  A logit of +inf counts as the largest finite
+ * value.
+ * Without a bias and with one group the choice compares the logits
+ * themselves; otherwise scores and choice values are computed in fp64.
+ *   logits   [M, ldl] of ldt (CONVROT_F32 or CONVROT_BF16), element aligned,
+ *            E columns, 1 <= E <= 1024
+ *   bias     [E] fp32 or NULL
+ *   ids      [M, top_k] int32, weights [M, top_k] fp32, dense */
+convrot_status convrot_route(const void* logits, convrot_dtype ldt, int64_t ldl, int64_t M, int64_t E,
+                             const float* bias, const convrot_routing* rule, int32_t* ids, float* weights,
+                             void* stream);
+
+/* The plan of a batch's pairs, in caller-owned device memory:
+ *   order    [pairs] int32, the pairs by group, ascending inside a group;
+ *            the pairs without a group follow the last group
+ *   offsets  [groups + 1] int32: group g's pairs are at positions
+ *            offsets[g] .. offsets[g + 1] - 1 of the order
+ *   tiles    [convrot_row_groups_tiles(pairs, groups)] int32: the groups cut
+ *            into row tiles for the products, in a form of the library's own
+ *   pairs    0 to 2^22
+ *   groups   1 to 4096
+ *   per_row  k, a positive divisor of pairs */
+typedef struct {
+  int32_t* order;
+  int32_t* offsets;
+  int32_t* tiles;
+  int64_t pairs;
+  int32_t groups;
+  int32_t per_row;
+} convrot_row_groups;
+
+/* int32 values of convrot_row_groups.tiles. */
+convrot_status convrot_row_groups_tiles(int64_t pairs, int64_t groups, int64_t* count);
+
+/* Writes the plan of ids [pairs] (int32, dense) into out's buffers.  A stable
+ * counting sort without atomics across workgroups: the same ids give the
+ * same plan.  One launch up to 8192 pairs, two above.  A plan serves any
+ * number of calls; a call that reads it must be ordered behind this one. */
+convrot_status convrot_group_rows(const int32_t* ids, const convrot_row_groups* out, void* stream);
+
+/* Which row of an operand belongs to position i of a plan's order, with
+ * pair p = order[i]. */
+typedef enum {
+  CONVROT_BY_ROW = 0,  /* row p / per_row: every pair of a row reads the same one (inputs only) */
+  CONVROT_BY_PAIR = 1, /* row p */
+  CONVROT_SORTED = 2   /* row i: groups are consecutive */
+} convrot_row_order;
+
+/* The quantised linear whose rows meet the weight of their group:
+ *   Y[dest] = fn(A[x, o] * act->scale[x] * w->scale[e N + o] + bias[e N + o])
+ * for every pair with a group e, x its row of `act` and dest its row of Y.
+ *   act     packed activation, ROWS layout; pairs / per_row rows with
+ *           source CONVROT_BY_ROW, else pairs rows
+ *   w       packed weights stacked over the groups, [groups * N, K], ROWS
+ *           layout; same K and rotation as `act` (CONVROT_ERR_MISMATCH
+ *           otherwise)
+ *   bias    [groups * N] fp32 or NULL
+ *   fn      CONVROT_ACT_NONE, _GELU_ERF, _GELU_TANH or _SILU
+ *   groups  a plan
+ *   source  any convrot_row_order;  dest  CONVROT_BY_PAIR or CONVROT_SORTED
+ *   Y       [pairs, ldy] of ydt, CONVROT_F32 or CONVROT_BF16, element
+ *           aligned.  Rows of pairs without a group are left as they were
+ *           (CONVROT_SORTED: the rows behind offsets[groups]).
+ * The accumulator is exact and the epilogue that of convrot_linear and
+ * convrot_linear_act: a group's rows carry the bits those give for its
+ * weight alone.  Needs no workspace. */
+convrot_status convrot_linear_grouped(const convrot_packed* act, const convrot_packed* w, const float* bias,
+                                      convrot_act fn, const convrot_row_groups* groups, convrot_row_order source,
+                                      convrot_row_order dest, void* Y, convrot_dtype ydt, int64_t ldy,
+                                      void* stream);
+
+/* The gated pair over stacked weights, in one launch:
+ *   Y[dest] = fn(gate) * up
+ * with gate and up as convrot_linear_grouped computes them; fn is
+ * CONVROT_ACT_GELU_ERF, _GELU_TANH or _SILU; w_gate and w_up have the same
+ * rows (CONVROT_ERR_MISMATCH otherwise). */
+convrot_status convrot_linear_gated_grouped(const convrot_packed* act, const convrot_packed* w_gate,
+                                            const float* b_gate, const convrot_packed* w_up, const float* b_up,
+                                            convrot_act fn, const convrot_row_groups* groups,
+                                            convrot_row_order source, convrot_row_order dest, void* Y,
+                                            convrot_dtype ydt, int64_t ldy, void* stream);
+
+/* The weighted sum that undoes the routing:
+ *   out[m, :] = sum_j weights[m, j] Y[m k + j, :]
+ * over the pairs whose id is in [0, groups), in the order of j, in fp32,
+ * rounded once.  Rows of Y of other pairs are not read; a row without any
+ * such pair becomes zero.
+ *   Y        [M * k, ldy] of dt, CONVROT_F32 or CONVROT_BF16 (by pair)
+ *   weights  [M, k] fp32, ids [M, k] int32, dense
+ *   out      [M, ldo] of dt; must not overlap Y.  M * k at most 2^22. */
+convrot_status convrot_combine_rows(const void* Y, convrot_dtype dt, int64_t ldy, const float* weights,
+                                    const int32_t* ids, int64_t M, int64_t k, int64_t N, int64_t groups, void* out,
+                                    int64_t ldo, void* stream);
+
+/* convrot_lora_add for a batch whose rows use different adapters.  With g
+ * the group of row m:
+ *   T[m] = X[m] A_g^T                     fp32 sums
+ *   out[m, n] = Y[m, n] + scales[g] * sum_j T[m, j] B_g[n, j]
+ * and out[m] = Y[m] for a row without a group (not touched where out is Y).
+ * T is not rounded to bf16: it enters the second product as the sum of two
+ * bf16 terms (bf16 Y) or three (fp32 Y).
+ *   X        [M, ldx] bf16, unrotated; A [groups][r, lda] and
+ *            B [groups][N, ldb] bf16, stacked stride_a and stride_b elements
+ *            apart (at least r * lda, N * ldb); adapters of lower rank
+ *            are padded with zeros in both
+ *   scales   [groups] fp32, on the device
+ *   r        a positive multiple of 16, at most 256; K a positive multiple
+ *            of 16
+ *   groups   a plan with per_row 1 and M pairs
+ *   Y, out   [M, ldy], [M, ldo] of dt, CONVROT_F32 or CONVROT_BF16; out is Y
+ *            (with ldo == ldy) or does not overlap it
+ *   workspace  16-byte aligned, at least
+ *            convrot_lora_grouped_workspace_bytes(...) bytes; not shared
+ *            with a concurrent call
+ * X, A and B: 16-byte aligned bases, rows and stacks.  Two launches. */
+convrot_status convrot_lora_grouped_workspace_bytes(int64_t M, int64_t K, int64_t r, int64_t groups,
+                                                    int64_t* bytes);
+
+convrot_status convrot_lora_add_grouped(const void* X, int64_t ldx, int64_t M, int64_t K, const void* A, int64_t lda,
+                                        int64_t stride_a, const void* B, int64_t ldb, int64_t stride_b, int64_t N,
+                                        int64_t r, const float* scales, const convrot_row_groups* groups,
+                                        const void* Y, int64_t ldy, convrot_dtype dt, void* out, int64_t ldo,
+                                        void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* convrot_status_string(convrot_status status);

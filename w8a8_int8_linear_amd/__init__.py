@@ -13,5 +13,9 @@ from .api import (  # noqa: F401
     lora_add, lora_workspace_bytes, pack_act, pack_act_rowmax, pack_weight, pack_weight_w4, rotate, smooth_ffn,
     tile_weight, tile_weight_w4, unpack_w4,
 )
-from .layer import ConvRotLinear, Route, RoutingLog  # noqa: F401
+from .layer import ConvRotExperts, ConvRotLinear, Route, RoutingLog  # noqa: F401
+from .routed import (  # noqa: F401
+    BY_PAIR, BY_ROW, SIGMOID, SILU, SOFTMAX, SORTED, RowGroups, combine_rows, group_rows, linear_gated_grouped,
+    linear_grouped, lora_add_grouped, lora_grouped_workspace_bytes, route, row_groups_tiles,
+)
 from ._lib import ConvrotError  # noqa: F401

@@ -12,7 +12,7 @@ import threading
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libconvrot.so")
 
-ABI_VERSION = 10
+ABI_VERSION = 11
 NOALLOC_SCRATCH_BYTES = 1 << 20
 
 # convrot_status
@@ -22,12 +22,16 @@ F32, BF16, I32 = 0, 1, 2
 # convrot_rot_kind
 ROT_REGULAR, ROT_RANDOMIZED = 0, 1
 # convrot_act
-ACT_NONE, ACT_GELU_ERF, ACT_GELU_TANH = 0, 1, 2
+ACT_NONE, ACT_GELU_ERF, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3
 # convrot_smooth_norm
 SMOOTH_L2, SMOOTH_MAX = 0, 1
 # convrot_linear_kind (workspace queries)
 LINEAR_PLAIN, LINEAR_GATED, LINEAR_BF16, LINEAR_W4, LINEAR_W4_GATED = range(5)
 LAYOUT_ROWS, LAYOUT_TILE16 = 0, 1
+# convrot_score
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+# convrot_row_order
+BY_ROW, BY_PAIR, SORTED = range(3)
 
 EXPORTED = (
     "convrot_pack_act",
@@ -52,6 +56,14 @@ EXPORTED = (
     "convrot_smooth_ffn",
     "convrot_lora_workspace_bytes",
     "convrot_lora_add",
+    "convrot_route",
+    "convrot_row_groups_tiles",
+    "convrot_group_rows",
+    "convrot_linear_grouped",
+    "convrot_linear_gated_grouped",
+    "convrot_combine_rows",
+    "convrot_lora_grouped_workspace_bytes",
+    "convrot_lora_add_grouped",
     "convrot_status_string",
     "convrot_last_error",
     "convrot_abi_version",
@@ -83,6 +95,28 @@ class PackedW4(ctypes.Structure):
         ("ld", ctypes.c_int64),
         ("rot", Rot),
         ("layout", ctypes.c_int32),
+    ]
+
+
+class Routing(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class RowGroups(ctypes.Structure):
+    _fields_ = [
+        ("order", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p),
+        ("tiles", ctypes.c_void_p),
+        ("pairs", ctypes.c_int64),
+        ("groups", ctypes.c_int32),
+        ("per_row", ctypes.c_int32),
     ]
 
 
@@ -147,6 +181,24 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.convrot_lora_add.argtypes = [vp, c_i64, c_i64, c_i64, vp, c_i64, vp, c_i64, c_i64, c_i64, ctypes.c_float, vp,
                                      c_int, c_i64, vp, c_i64, vp]
     lib.convrot_lora_add.restype = c_int
+    PG = ctypes.POINTER(RowGroups)
+    lib.convrot_route.argtypes = [vp, c_int, c_i64, c_i64, c_i64, vp, ctypes.POINTER(Routing), vp, vp, vp]
+    lib.convrot_route.restype = c_int
+    lib.convrot_row_groups_tiles.argtypes = [c_i64, c_i64, ctypes.POINTER(c_i64)]
+    lib.convrot_row_groups_tiles.restype = c_int
+    lib.convrot_group_rows.argtypes = [vp, PG, vp]
+    lib.convrot_group_rows.restype = c_int
+    lib.convrot_linear_grouped.argtypes = [P, P, vp, c_int, PG, c_int, c_int, vp, c_int, c_i64, vp]
+    lib.convrot_linear_grouped.restype = c_int
+    lib.convrot_linear_gated_grouped.argtypes = [P, P, vp, P, vp, c_int, PG, c_int, c_int, vp, c_int, c_i64, vp]
+    lib.convrot_linear_gated_grouped.restype = c_int
+    lib.convrot_combine_rows.argtypes = [vp, c_int, c_i64, vp, vp, c_i64, c_i64, c_i64, c_i64, vp, c_i64, vp]
+    lib.convrot_combine_rows.restype = c_int
+    lib.convrot_lora_grouped_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i64, ctypes.POINTER(c_i64)]
+    lib.convrot_lora_grouped_workspace_bytes.restype = c_int
+    lib.convrot_lora_add_grouped.argtypes = [vp, c_i64, c_i64, c_i64, vp, c_i64, c_i64, vp, c_i64, c_i64, c_i64, c_i64,
+                                             vp, PG, vp, c_i64, c_int, vp, c_i64, vp, c_i64, vp]
+    lib.convrot_lora_add_grouped.restype = c_int
     lib.convrot_status_string.argtypes = [c_int]
     lib.convrot_status_string.restype = ctypes.c_char_p
     lib.convrot_last_error.argtypes = []

@@ -3,6 +3,7 @@
 // The declarations and the contract of every entry point are in convrot.h.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -195,8 +196,9 @@ convrot_status pack_impl(const char* what, const void* X, convrot_dtype xdt, int
 
 // Checks shared by the quantised linear entry points: a packed activation
 // and a packed weight that belong together, a bias and an output of Y.
+// (check_y false: the caller checks Y itself).
 convrot_status check_linear(const char* fn, const convrot_packed* act, const convrot_packed* w, const float* bias,
-                            const void* Y, convrot_dtype ydt, int64_t ldy, bool i32_ok) {
+                            const void* Y, convrot_dtype ydt, int64_t ldy, bool i32_ok, bool check_y = true) {
   int lga = 0, lgw = 0;
   convrot_status st = check_packed("activation", act, &lga, true);
   if (st != CONVROT_OK) return st;
@@ -218,8 +220,10 @@ convrot_status check_linear(const char* fn, const convrot_packed* act, const con
   if (ydt != CONVROT_F32 && ydt != CONVROT_BF16 && !(i32_ok && ydt == CONVROT_I32))
     return fail(CONVROT_ERR_DTYPE, "%s: output must be CONVROT_F32 or CONVROT_BF16%s", fn,
                 i32_ok ? " or CONVROT_I32" : "");
-  st = check_matrix("Y", Y, act->rows, w->rows, ldy, elt_size(ydt), false);
-  if (st != CONVROT_OK) return st;
+  if (check_y) {
+    st = check_matrix("Y", Y, act->rows, w->rows, ldy, elt_size(ydt), false);
+    if (st != CONVROT_OK) return st;
+  }
   if (bias != nullptr && (reinterpret_cast<uintptr_t>(bias) & 3u) != 0)
     return fail(CONVROT_ERR_ALIGN, "bias must be 4-byte aligned");
   if (act->ld > kMaxLdBytes || w->ld > kMaxLdBytes)
@@ -910,6 +914,279 @@ convrot_status convrot_lora_add(const void* X, int64_t ldx, int64_t M, int64_t K
   if (e == hipSuccess)
     e = convrot::launch_lora_up(workspace, r, B, ldb, M, N, r, scale, Y, static_cast<convrot::Elt>(ydt), ldy, s);
   return from_hip(e, what);
+}
+
+namespace {
+// Checks of a plan; `what` names the entry point.
+convrot_status check_groups(const char* what, const convrot_row_groups* g) {
+  if (g == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: row groups descriptor is NULL", what);
+  if (g->pairs < 0 || g->pairs > convrot::kPlanMaxPairs)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: pairs = %lld must be 0 to %lld", what, static_cast<long long>(g->pairs),
+                static_cast<long long>(convrot::kPlanMaxPairs));
+  if (g->groups < 1 || g->groups > convrot::kPlanMaxGroups)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: groups = %d must be 1 to %lld", what, g->groups,
+                static_cast<long long>(convrot::kPlanMaxGroups));
+  if (g->per_row < 1 || g->pairs % g->per_row != 0)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: per_row = %d must be a positive divisor of pairs = %lld", what,
+                g->per_row, static_cast<long long>(g->pairs));
+  if ((g->pairs > 0 && g->order == nullptr) || g->offsets == nullptr || g->tiles == nullptr)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: a buffer of the row groups is NULL", what);
+  for (const int32_t* p : {g->order, g->offsets, g->tiles})
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+      return fail(CONVROT_ERR_ALIGN, "%s: the row groups' buffers must be 4-byte aligned", what);
+  return CONVROT_OK;
+}
+
+convrot::RowPlan row_plan(const convrot_row_groups* g) {
+  return convrot::RowPlan{g->order, g->offsets, g->tiles, g->pairs, g->groups, g->per_row};
+}
+
+// A grid of workgroups counted in one dimension.
+convrot_status check_grid(const char* what, int64_t blocks) {
+  if (blocks > kMaxRows)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: the problem needs %lld workgroups, more than one launch holds", what,
+                static_cast<long long>(blocks));
+  return CONVROT_OK;
+}
+
+// Checks of one weight of a grouped linear: as check_linear, with the row
+// counts of a plan in place of M and N.
+convrot_status check_grouped(const char* what, const convrot_packed* act, const convrot_packed* w, const float* bias,
+                             const convrot_row_groups* g, convrot_row_order source, convrot_row_order dest,
+                             const void* Y, convrot_dtype ydt, int64_t ldy) {
+  convrot_status st = check_groups(what, g);
+  if (st != CONVROT_OK) return st;
+  if (source != CONVROT_BY_ROW && source != CONVROT_BY_PAIR && source != CONVROT_SORTED)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: unknown source order %d", what, static_cast<int>(source));
+  if (dest != CONVROT_BY_PAIR && dest != CONVROT_SORTED)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: the output order must be CONVROT_BY_PAIR or CONVROT_SORTED", what);
+  int lg = 0;
+  st = check_packed("weight", w, &lg);
+  if (st != CONVROT_OK) return st;
+  if (w->rows % g->groups != 0)
+    return fail(CONVROT_ERR_MISMATCH, "%s: the weight has %lld rows, not a multiple of the %d groups", what,
+                static_cast<long long>(w->rows), g->groups);
+  st = check_rows_layout("weight", w->layout);
+  if (st != CONVROT_OK) return st;
+  // K, rotation and types; Y is checked below with its own row and column counts.
+  st = check_linear(what, act, w, bias, nullptr, ydt, 0, false, false);
+  if (st != CONVROT_OK) return st;
+  st = check_rows_layout("activation", act->layout);
+  if (st != CONVROT_OK) return st;
+  const int64_t rows = source == CONVROT_BY_ROW ? g->pairs / g->per_row : g->pairs;
+  if (act->rows != rows)
+    return fail(CONVROT_ERR_MISMATCH, "%s: the activation has %lld rows, the row groups and their order need %lld",
+                what, static_cast<long long>(act->rows), static_cast<long long>(rows));
+  const int64_t N = w->rows / g->groups;
+  st = check_matrix("Y", Y, N > 0 ? g->pairs : 0, N, ldy, elt_size(ydt), false);
+  if (st != CONVROT_OK) return st;
+  return check_grid(what, convrot::plan_max_tiles(g->pairs, g->groups, 0) * ((N + 15) / 16));
+}
+}  // namespace
+
+convrot_status convrot_route(const void* logits, convrot_dtype ldt, int64_t ldl, int64_t M, int64_t E,
+                             const float* bias, const convrot_routing* rule, int32_t* ids, float* weights,
+                             void* stream) {
+  const char* what = "convrot_route";
+  if (rule == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: rule is NULL", what);
+  if (E < 1 || E > convrot::kRouteMaxExperts)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: E = %lld must be 1 to %lld", what, static_cast<long long>(E),
+                static_cast<long long>(convrot::kRouteMaxExperts));
+  if (ldt != CONVROT_F32 && ldt != CONVROT_BF16)
+    return fail(CONVROT_ERR_DTYPE, "%s: logits must be CONVROT_F32 or CONVROT_BF16", what);
+  if (rule->score != CONVROT_SCORE_SOFTMAX && rule->score != CONVROT_SCORE_SIGMOID)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: unknown score %d", what, rule->score);
+  if (rule->groups < 1 || rule->groups > 64 || E % rule->groups != 0)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: groups = %d must be 1 to 64 and divide E = %lld", what, rule->groups,
+                static_cast<long long>(E));
+  if (rule->top_groups < 1 || rule->top_groups > rule->groups)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: top_groups = %d must be 1 to groups = %d", what, rule->top_groups,
+                rule->groups);
+  if (rule->top_k < 1 || rule->top_k > convrot::kRouteMaxChoices ||
+      rule->top_k > E / rule->groups * rule->top_groups)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: top_k = %d must be 1 to 64 and at most the %lld experts of the kept groups",
+                what, rule->top_k, static_cast<long long>(E / rule->groups * rule->top_groups));
+  convrot_status st = check_matrix("logits", logits, M, E, ldl, elt_size(ldt), false);
+  if (st != CONVROT_OK) return st;
+  if (M > 0 && (ids == nullptr || weights == nullptr))
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: ids or weights is NULL", what);
+  for (const void* p : {static_cast<const void*>(bias), static_cast<const void*>(ids), static_cast<const void*>(weights)})
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0)
+      return fail(CONVROT_ERR_ALIGN, "%s: bias, ids and weights must be 4-byte aligned", what);
+  if (M == 0) return ok();
+  convrot::RouteArgs ra{};
+  ra.k = rule->top_k;
+  ra.groups = rule->groups;
+  ra.top_groups = rule->top_groups;
+  ra.sigmoid = rule->score == CONVROT_SCORE_SIGMOID;
+  ra.renormalise = rule->renormalise != 0;
+  ra.scale = rule->scale;
+  return from_hip(convrot::launch_route(logits, static_cast<convrot::Elt>(ldt), ldl, M, E, bias, ra, ids, weights,
+                                        static_cast<hipStream_t>(stream)),
+                  what);
+}
+
+convrot_status convrot_row_groups_tiles(int64_t pairs, int64_t groups, int64_t* count) {
+  const char* what = "convrot_row_groups_tiles";
+  if (count == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: count is NULL", what);
+  if (pairs < 0 || pairs > convrot::kPlanMaxPairs || groups < 1 || groups > convrot::kPlanMaxGroups)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: pairs must be 0 to %lld and groups 1 to %lld", what,
+                static_cast<long long>(convrot::kPlanMaxPairs), static_cast<long long>(convrot::kPlanMaxGroups));
+  *count = convrot::plan_ints(pairs, groups);
+  return ok();
+}
+
+convrot_status convrot_group_rows(const int32_t* ids, const convrot_row_groups* out, void* stream) {
+  const char* what = "convrot_group_rows";
+  convrot_status st = check_groups(what, out);
+  if (st != CONVROT_OK) return st;
+  if (out->pairs > 0 && ids == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: ids is NULL", what);
+  if ((reinterpret_cast<uintptr_t>(ids) & 3u) != 0) return fail(CONVROT_ERR_ALIGN, "%s: ids must be 4-byte aligned", what);
+  return from_hip(convrot::launch_group_rows(ids, out->pairs, out->groups, out->order, out->offsets, out->tiles,
+                                             static_cast<hipStream_t>(stream)),
+                  what);
+}
+
+convrot_status convrot_linear_grouped(const convrot_packed* act, const convrot_packed* w, const float* bias,
+                                      convrot_act fn, const convrot_row_groups* groups, convrot_row_order source,
+                                      convrot_row_order dest, void* Y, convrot_dtype ydt, int64_t ldy,
+                                      void* stream) {
+  const char* what = "convrot_linear_grouped";
+  if (fn < CONVROT_ACT_NONE || fn > CONVROT_ACT_SILU)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: unknown activation %d", what, static_cast<int>(fn));
+  const convrot_status st = check_grouped(what, act, w, bias, groups, source, dest, Y, ydt, ldy);
+  if (st != CONVROT_OK) return st;
+  const convrot::RowPlan plan = row_plan(groups);
+  return from_hip(convrot::launch_linear_grouped(
+                      act->q, act->ld, w->q, w->ld, act->scale, w->scale, bias, nullptr, 0, nullptr, nullptr, false,
+                      static_cast<convrot::Act>(fn), plan, static_cast<convrot::RowOrder>(source),
+                      static_cast<convrot::RowOrder>(dest), w->rows / groups->groups, act->K, Y,
+                      static_cast<convrot::Elt>(ydt), ldy, static_cast<hipStream_t>(stream)),
+                  what);
+}
+
+convrot_status convrot_linear_gated_grouped(const convrot_packed* act, const convrot_packed* w_gate,
+                                            const float* b_gate, const convrot_packed* w_up, const float* b_up,
+                                            convrot_act fn, const convrot_row_groups* groups,
+                                            convrot_row_order source, convrot_row_order dest, void* Y,
+                                            convrot_dtype ydt, int64_t ldy, void* stream) {
+  const char* what = "convrot_linear_gated_grouped";
+  if (fn < CONVROT_ACT_GELU_ERF || fn > CONVROT_ACT_SILU)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: activation must be CONVROT_ACT_GELU_ERF, _GELU_TANH or _SILU", what);
+  convrot_status st = check_grouped(what, act, w_gate, b_gate, groups, source, dest, Y, ydt, ldy);
+  if (st != CONVROT_OK) return st;
+  if (w_up != nullptr && w_gate->rows != w_up->rows)
+    return fail(CONVROT_ERR_MISMATCH, "gate has %lld output rows but up has %lld",
+                static_cast<long long>(w_gate->rows), static_cast<long long>(w_up->rows));
+  st = check_grouped(what, act, w_up, b_up, groups, source, dest, Y, ydt, ldy);
+  if (st != CONVROT_OK) return st;
+  const convrot::RowPlan plan = row_plan(groups);
+  return from_hip(convrot::launch_linear_grouped(
+                      act->q, act->ld, w_gate->q, w_gate->ld, act->scale, w_gate->scale, b_gate, w_up->q, w_up->ld,
+                      w_up->scale, b_up, true, static_cast<convrot::Act>(fn), plan,
+                      static_cast<convrot::RowOrder>(source), static_cast<convrot::RowOrder>(dest),
+                      w_gate->rows / groups->groups, act->K, Y, static_cast<convrot::Elt>(ydt), ldy,
+                      static_cast<hipStream_t>(stream)),
+                  what);
+}
+
+convrot_status convrot_combine_rows(const void* Y, convrot_dtype dt, int64_t ldy, const float* weights,
+                                    const int32_t* ids, int64_t M, int64_t k, int64_t N, int64_t groups, void* out,
+                                    int64_t ldo, void* stream) {
+  const char* what = "convrot_combine_rows";
+  if (dt != CONVROT_F32 && dt != CONVROT_BF16)
+    return fail(CONVROT_ERR_DTYPE, "%s: Y and out must be CONVROT_F32 or CONVROT_BF16", what);
+  if (M < 0 || k < 1 || N < 0 || M > convrot::kPlanMaxPairs || k > convrot::kPlanMaxPairs ||
+      M * k > convrot::kPlanMaxPairs)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: bad sizes (M * k at most %lld, k at least 1)", what,
+                static_cast<long long>(convrot::kPlanMaxPairs));
+  if (groups < 1 || groups > convrot::kPlanMaxGroups)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: groups = %lld must be 1 to %lld", what, static_cast<long long>(groups),
+                static_cast<long long>(convrot::kPlanMaxGroups));
+  if (N > kMaxRows) return fail(CONVROT_ERR_INVALID_ARG, "%s: bad N", what);
+  convrot_status st = check_matrix("Y", Y, M * k, N, ldy, elt_size(dt), false);
+  if (st != CONVROT_OK) return st;
+  st = check_matrix("out", out, M, N, ldo, elt_size(dt), false);
+  if (st != CONVROT_OK) return st;
+  if (M > 0 && (weights == nullptr || ids == nullptr))
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: weights or ids is NULL", what);
+  if ((reinterpret_cast<uintptr_t>(weights) & 3u) != 0 || (reinterpret_cast<uintptr_t>(ids) & 3u) != 0)
+    return fail(CONVROT_ERR_ALIGN, "%s: weights and ids must be 4-byte aligned", what);
+  st = check_grid(what, M * ((N + 255) / 256));
+  if (st != CONVROT_OK) return st;
+  return from_hip(convrot::launch_combine_rows(Y, static_cast<convrot::Elt>(dt), ldy, weights, ids, M, k, N, groups,
+                                               out, ldo, static_cast<hipStream_t>(stream)),
+                  what);
+}
+
+convrot_status convrot_lora_grouped_workspace_bytes(int64_t M, int64_t K, int64_t r, int64_t groups,
+                                                    int64_t* bytes) {
+  const char* what = "convrot_lora_grouped_workspace_bytes";
+  if (bytes == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: bytes is NULL", what);
+  const convrot_status st = check_lora_shape(what, M, K, r);
+  if (st != CONVROT_OK) return st;
+  if (M > convrot::kPlanMaxPairs || groups < 1 || groups > convrot::kPlanMaxGroups)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: M must be at most %lld and groups 1 to %lld", what,
+                static_cast<long long>(convrot::kPlanMaxPairs), static_cast<long long>(convrot::kPlanMaxGroups));
+  *bytes = convrot::lora_grouped_ws_bytes(M, K, r, groups);
+  return ok();
+}
+
+convrot_status convrot_lora_add_grouped(const void* X, int64_t ldx, int64_t M, int64_t K, const void* A, int64_t lda,
+                                        int64_t stride_a, const void* B, int64_t ldb, int64_t stride_b, int64_t N,
+                                        int64_t r, const float* scales, const convrot_row_groups* groups,
+                                        const void* Y, int64_t ldy, convrot_dtype dt, void* out, int64_t ldo,
+                                        void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* what = "convrot_lora_add_grouped";
+  convrot_status st = check_lora_shape(what, M, K, r);
+  if (st != CONVROT_OK) return st;
+  st = check_groups(what, groups);
+  if (st != CONVROT_OK) return st;
+  if (groups->per_row != 1 || groups->pairs != M)
+    return fail(CONVROT_ERR_MISMATCH, "%s: the row groups must hold one pair per row (per_row 1, %lld pairs)", what,
+                static_cast<long long>(M));
+  if (N < 0 || N > kMaxRows) return fail(CONVROT_ERR_INVALID_ARG, "%s: bad N", what);
+  if (dt != CONVROT_F32 && dt != CONVROT_BF16)
+    return fail(CONVROT_ERR_DTYPE, "%s: Y and out must be CONVROT_F32 or CONVROT_BF16", what);
+  st = check_matrix("X", X, M, K, ldx, 2);
+  if (st != CONVROT_OK) return st;
+  st = check_matrix("A", A, r, K, lda, 2);
+  if (st != CONVROT_OK) return st;
+  st = check_matrix("B", B, N, r, ldb, 2);
+  if (st != CONVROT_OK) return st;
+  st = check_matrix("Y", Y, M, N, ldy, elt_size(dt), false);
+  if (st != CONVROT_OK) return st;
+  st = check_matrix("out", out, M, N, ldo, elt_size(dt), false);
+  if (st != CONVROT_OK) return st;
+  if (2 * ldx > kMaxLdBytes || 2 * lda > kMaxLdBytes)
+    return fail(CONVROT_ERR_INVALID_ARG, "leading dimension of X or A exceeds %lld bytes",
+                static_cast<long long>(kMaxLdBytes));
+  if (stride_a < r * lda || stride_b / ldb < N)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: adapters overlap (stride_a < r * lda or stride_b < N * ldb)", what);
+  if ((2 * stride_a) % 16 != 0 || (2 * stride_b) % 16 != 0)
+    return fail(CONVROT_ERR_ALIGN, "%s: the adapters must lie a multiple of 16 bytes apart", what);
+  if (M == 0 || N == 0) return ok();
+  if (scales == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: scales is NULL", what);
+  if ((reinterpret_cast<uintptr_t>(scales) & 3u) != 0)
+    return fail(CONVROT_ERR_ALIGN, "%s: scales must be 4-byte aligned", what);
+  if (out == Y) {
+    if (ldo != ldy) return fail(CONVROT_ERR_INVALID_ARG, "%s: out is Y but ldo != ldy", what);
+  } else {
+    const auto* y = static_cast<const char*>(Y);
+    const auto* o = static_cast<const char*>(out);
+    const int64_t elt = elt_size(dt);
+    if (y < o + ((M - 1) * ldo + N) * elt && o < y + ((M - 1) * ldy + N) * elt)
+      return fail(CONVROT_ERR_INVALID_ARG, "%s: out overlaps Y without being Y", what);
+  }
+  st = check_workspace(workspace, workspace_bytes, convrot::lora_grouped_ws_bytes(M, K, r, groups->groups));
+  if (st != CONVROT_OK) return st;
+  // the second product's grid, the larger of the two
+  st = check_grid(what, convrot::plan_max_tiles(M, groups->groups, 0) * std::max<int64_t>((N + 63) / 64, 32));
+  if (st != CONVROT_OK) return st;
+  return from_hip(convrot::launch_lora_grouped(X, ldx, A, lda, stride_a, B, ldb, stride_b, scales, M, K, N, r,
+                                               row_plan(groups), Y, ldy, out, ldo, static_cast<convrot::Elt>(dt),
+                                               workspace, static_cast<hipStream_t>(stream)),
+                  what);
 }
 
 const char* convrot_status_string(convrot_status status) {

@@ -10,7 +10,7 @@ namespace convrot {
 enum class Elt : int { F32 = 0, BF16 = 1, I32 = 2 };
 enum class RotKind : int { Regular = 0, Randomized = 1 };
 // Activation of a fused epilogue (values of convrot_act).
-enum class Act : int { None = 0, GeluErf = 1, GeluTanh = 2 };
+enum class Act : int { None = 0, GeluErf = 1, GeluTanh = 2, Silu = 3 };
 
 // Fused group rotation + whole-row absmax + int8 quantisation of `rows` rows
 // of X.  When `q` is null the kernel writes the fp32 rotated rows to `xrot`
@@ -169,5 +169,84 @@ hipError_t launch_gemv_w4_gated(const int8_t* A, int64_t lda, const uint8_t* Bg,
                                 const float* biasg, const uint8_t* Bu, int64_t ldbu, const float* sbu,
                                 const float* biasu, const float* sa, Act act, int64_t M, int64_t N, int64_t K,
                                 void* C, Elt out, int64_t ldc, void* ws, hipStream_t stream, bool tiled = false);
+
+// ---------------------------------------------------------------------------
+// Rows that choose their weights
+// ---------------------------------------------------------------------------
+
+// The router's rule (convrot_routing); per_group and log2_lanes are set by
+// the launcher.
+struct RouteArgs {
+  int k;
+  int groups;
+  int top_groups;
+  bool sigmoid;
+  bool renormalise;
+  float scale;
+  int per_group;   // experts per group
+  int log2_lanes;  // log2 of the lanes that share a group's value
+};
+constexpr int64_t kRouteMaxExperts = 1024;
+constexpr int64_t kRouteMaxChoices = 64;  // one lane keeps each choice
+hipError_t launch_route(const void* logits, Elt dt, int64_t ldl, int64_t M, int64_t E, const float* bias,
+                        RouteArgs ra, int32_t* ids, float* weights, hipStream_t stream);
+
+// The plan of pairs grouped by id.  `tiles` starts with kPlanLists counts of
+// grouped tiles and kPlanLists counts of all tiles, then list b (tiles of
+// 16 << b positions, {group, first position} each) at plan_list_at(.., b);
+// the ungrouped positions are group E.
+constexpr int kPlanLists = 5;
+constexpr int64_t kPlanMaxChunks = 256;
+constexpr int64_t kPlanMaxPairs = int64_t{1} << 22;
+constexpr int64_t kPlanMaxGroups = 4096;
+// Most tiles of 16 << b positions: every non-empty group adds at most one
+// that is not full.
+__host__ __device__ inline int64_t plan_max_tiles(int64_t pairs, int64_t E, int b) {
+  return pairs / (16 << b) + (E + 1 < pairs ? E + 1 : pairs);
+}
+__host__ __device__ inline int64_t plan_list_at(int64_t pairs, int64_t E, int b) {
+  int64_t at = 2 * kPlanLists;
+  for (int i = 0; i < b; ++i) at += 2 * plan_max_tiles(pairs, E, i);
+  return at;
+}
+int64_t plan_ints(int64_t pairs, int64_t E);  // int32 values of `tiles`
+hipError_t launch_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32_t* order, int32_t* offsets,
+                             int32_t* tiles, hipStream_t stream);
+
+// out[m] = sum_j weights[m, j] Y[m k + j] over pairs whose id is in [0, E).
+hipError_t launch_combine_rows(const void* Y, Elt dt, int64_t ldy, const float* weights, const int32_t* ids,
+                               int64_t M, int64_t k, int64_t N, int64_t E, void* out, int64_t ldo,
+                               hipStream_t stream);
+
+// A plan as the products read it: pair p of row p / per_row sits at position
+// i with order[i] = p.
+struct RowPlan {
+  const int32_t* order;
+  const int32_t* offsets;
+  const int32_t* tiles;
+  int64_t pairs;
+  int groups;
+  int per_row;
+};
+// Which row of an operand belongs to a position (convrot_row_order).
+enum class RowOrder : int { Row = 0, Pair = 1, Sorted = 2 };
+
+// Grouped linears over stacked weights [groups * N, K]: the rows of group e
+// meet weight rows e N .. (e + 1) N - 1.
+//   plain  Y = act(A sa sb + bias)            (act None; Gelu; Silu)
+//   gated  Y = act(A sa sb + bias) * (A sa sb2 + bias2)  with epi.B2
+hipError_t launch_linear_grouped(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* sa,
+                                 const float* sb, const float* bias, const int8_t* B2, int64_t ldb2, const float* sb2,
+                                 const float* bias2, bool gated, Act act, const RowPlan& plan, RowOrder source,
+                                 RowOrder dest, int64_t N, int64_t K, void* C, Elt out, int64_t ldc,
+                                 hipStream_t stream);
+
+// Low-rank corrections of rows in different groups: T = X A_g^T into the
+// workspace, then out = Y + scale_g T B_g^T.
+int64_t lora_grouped_ws_bytes(int64_t M, int64_t K, int64_t r, int64_t E);
+hipError_t launch_lora_grouped(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t stride_a,
+                               const void* B, int64_t ldb, int64_t stride_b, const float* scales, int64_t M,
+                               int64_t K, int64_t N, int64_t r, const RowPlan& plan, const void* Y, int64_t ldy,
+                               void* out, int64_t ldo, Elt dt, void* ws, hipStream_t stream);
 
 }  // namespace convrot

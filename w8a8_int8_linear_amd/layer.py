@@ -20,6 +20,12 @@ further and runs them as one launch over their stacked packed weights.
 Weights are packed row by row, so stacking packed weights equals packing the
 stacked weights, and each layer's output is a column slice of the merged
 output (``split``).
+
+Batches whose requests have adapters of their own use a bank of stacked
+adapters (``set_lora_bank``) and the plan of the rows' adapter ids
+(``routed.group_rows``), passed with each call.  ``ConvRotExperts`` is the
+gated feed-forward layer of a mixture of experts: router, grouped int8
+products, weighted sum.
 """
 
 from __future__ import annotations
@@ -29,7 +35,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import api
+from . import api, routed
 
 log = logging.getLogger("w8a8_int8_linear_amd")
 
@@ -82,6 +88,7 @@ class ConvRotLinear:
         self.w_bf16 = w_bf16
         self.bias = bias
         self.adapters: list[tuple[torch.Tensor, torch.Tensor, float]] = []
+        self.bank: tuple[torch.Tensor, torch.Tensor, torch.Tensor] | None = None
         self.splits: list[int] = [N]
 
     @property
@@ -121,7 +128,7 @@ class ConvRotLinear:
         for l in layers:
             if not l.quantized:
                 raise ValueError(f"{l.name} is routed to bf16 and cannot be merged")
-            if l.adapters:
+            if l.adapters or l.bank is not None:
                 raise ValueError(f"{l.name} has LoRA adapters; merge the base layers, then attach adapters")
             if (l.K, l.group, l.kind, l.weight_bits) != (first.K, first.group, first.kind, first.weight_bits):
                 raise ValueError(f"{l.name} differs from {first.name} in K, group, rotation or weight width")
@@ -170,6 +177,17 @@ class ConvRotLinear:
             raise ValueError(f"adapter shapes must be a [r, {self.K}] and b [{self.N}, r]")
         self.adapters.append((a.to(torch.bfloat16).contiguous(), b.to(torch.bfloat16).contiguous(), float(scale)))
 
+    def set_lora_bank(self, a: torch.Tensor, b: torch.Tensor, scales: torch.Tensor) -> None:
+        """Attach adapters for batches whose rows use different ones: a
+        [n, r, K] (down) and b [n, N, r] (up) stacked, bf16, and scales [n].
+        A call then names its rows' adapters with ``groups``."""
+        n = a.shape[0]
+        if a.dim() != 3 or b.dim() != 3 or a.shape[2] != self.K or tuple(b.shape) != (n, self.N, a.shape[1]) or \
+                tuple(scales.shape) != (n,):
+            raise ValueError(f"bank shapes must be a [n, r, {self.K}], b [n, {self.N}, r] and scales [n]")
+        self.bank = (a.to(torch.bfloat16).contiguous(), b.to(torch.bfloat16).contiguous(),
+                     scales.to(torch.float32).contiguous())
+
     def _workspace(self, kind: str, M: int, device: torch.device) -> torch.Tensor | None:
         """The split-K workspace of a small-M call (a torch allocation of the
         caller's; None when the shape does not split).  Above 16 rows the
@@ -188,11 +206,16 @@ class ConvRotLinear:
         return api.pack_act(x.reshape(-1, self.K).contiguous(), self.group, self.kind,
                             self.packed.signs if self.packed is not None else None)
 
-    def __call__(self, x: torch.Tensor | api.Packed, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    def __call__(self, x: torch.Tensor | api.Packed, out_dtype: torch.dtype | None = None,
+                 groups: routed.RowGroups | None = None) -> torch.Tensor:
+        """``groups``: the plan of the rows' adapter ids into the layer's
+        bank (rows without a group get the base output)."""
+        if groups is not None and self.bank is None:
+            raise ValueError(f"{self.name} has no adapter bank for the row groups")
         if isinstance(x, api.Packed):
             if not self.quantized:
                 raise ValueError(f"{self.name} is routed to bf16 and cannot take a packed activation")
-            if self.adapters:
+            if self.adapters or groups is not None:
                 raise ValueError(f"{self.name} has LoRA adapters, which need the unrotated input, not a packed one")
             return self._linear(x, out_dtype or torch.bfloat16)
         shape = x.shape
@@ -203,8 +226,59 @@ class ConvRotLinear:
         else:
             y = api.linear_bf16(rows.to(torch.bfloat16), self.w_bf16, self.bias, dt,
                                 workspace=self._workspace(api.BF16, rows.shape[0], rows.device))
-        if self.adapters:
+        if self.adapters or groups is not None:
             xb = rows.to(torch.bfloat16).contiguous()
             for a, b, scale in self.adapters:
                 api.lora_add(xb, a, b, scale, y)
+            if groups is not None:
+                routed.lora_add_grouped(xb, *self.bank, y, groups)
         return y.reshape(*shape[:-1], self.N)
+
+
+class ConvRotExperts:
+    """The gated feed-forward layer of a mixture of experts on the packed
+    int8 path: bf16 router, choice of experts, grouped gate/up products,
+    pack, grouped down product, weighted sum.  The packed weights are stacked
+    over the experts; both widths must be multiples of the group size (there
+    is no bf16 path for experts)."""
+
+    def __init__(self, router: torch.Tensor, gate: api.Packed, up: api.Packed, down: api.Packed, top_k: int,
+                 score: str = routed.SOFTMAX, bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1,
+                 renormalise: bool = True, scale: float = 1.0, act: str = routed.SILU):
+        E, K = router.shape
+        if gate.rows != up.rows or gate.rows % E or down.rows % E or gate.K != K or up.K != K or \
+                down.K != gate.rows // E:
+            raise ValueError("router [E, K], gate and up [E * I, K] and down [E * N, I] do not fit")
+        self.router = router.to(torch.bfloat16).contiguous()
+        self.gate, self.up, self.down = gate, up, down
+        self.experts, self.K, self.inner, self.N = E, K, down.K, down.rows // E
+        self.rule = dict(top_k=top_k, score=score, bias=bias, groups=groups, top_groups=top_groups,
+                         renormalise=renormalise, scale=scale)
+        self.act = act
+
+    @classmethod
+    def from_dense(cls, router: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, top_k: int,
+                   group: int = 256, kind: str = api.REGULAR, signs: torch.Tensor | None = None,
+                   signs_down: torch.Tensor | None = None, **rule) -> "ConvRotExperts":
+        """Pack gate and up [E, I, K] and down [E, N, I] of every expert
+        (rotated with ``group``; ``signs`` [K] and ``signs_down`` [I] for the
+        randomized kind); ``rule`` as the constructor."""
+        def pack(w, s):
+            return api.pack_weight(w.reshape(-1, w.shape[-1]).contiguous(), group, kind, s)
+
+        return cls(router, pack(gate, signs), pack(up, signs), pack(down, signs_down), top_k, **rule)
+
+    def __call__(self, x: torch.Tensor, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+        shape = x.shape
+        rows = x.reshape(-1, self.K).contiguous()
+        dt = out_dtype or (x.dtype if x.dtype in (torch.float32, torch.bfloat16) else torch.bfloat16)
+        logits = api.linear_bf16(rows.to(torch.bfloat16), self.router, out_dtype=torch.float32)
+        ids, weights = routed.route(logits, **self.rule)
+        plan = routed.group_rows(ids, self.experts)
+        g = self.gate
+        h = routed.linear_gated_grouped(api.pack_act(rows, g.group, g.kind, g.signs), g, self.up, plan, act=self.act,
+                                        source=routed.BY_ROW, dest=routed.SORTED, out_dtype=torch.bfloat16)
+        d = self.down
+        y = routed.linear_grouped(api.pack_act(h, d.group, d.kind, d.signs), d, plan, source=routed.SORTED,
+                                  dest=routed.BY_PAIR, out_dtype=dt)
+        return routed.combine_rows(y, weights, ids, self.experts).reshape(*shape[:-1], self.N)
