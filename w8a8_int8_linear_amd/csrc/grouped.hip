@@ -56,7 +56,8 @@ struct GroupedArgs {
   int K;
   void* C;
   int64_t ldc;
-  int tiles_n;
+  int tiles_n;   // feature blocks
+  bool vec_out;  // rows of C take 16-byte stores
 };
 
 // SiLU, y / (1 + e^{-y}), with the hardware exp2 and reciprocal (at
@@ -105,6 +106,14 @@ __device__ __forceinline__ void store4(void* C, int64_t at, int n, int N, const 
     }
   }
 }
+
+}  // namespace
+}  // namespace convrot
+
+#include "grouped_tile.h"
+
+namespace convrot {
+namespace {
 
 template <int OUT, bool GATED, int MT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void grouped_stream_kernel(GroupedArgs a) {
@@ -215,6 +224,31 @@ hipError_t launch_stream(GroupedArgs a, const RowPlan& plan, hipStream_t stream)
   return hipGetLastError();
 }
 
+template <int OUT, bool GATED, bool KTAIL>
+hipError_t launch_tile_typed(GroupedArgs a, const RowPlan& plan, hipStream_t stream) {
+  auto kern = tile::grouped_tile_kernel<OUT, GATED, KTAIL>;
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), tile::kSmem, lds_set);
+  if (e != hipSuccess) return e;
+  constexpr int b = 4;  // tiles of 256 positions
+  a.list = plan.tiles + plan_list_at(plan.pairs, plan.groups, b);
+  a.count = plan.tiles + b;
+  constexpr int kFeat = GATED ? tile::kRows / 2 : tile::kRows;
+  a.tiles_n = (a.N + kFeat - 1) / kFeat;
+  const int elt = OUT == 0 ? 4 : 2;
+  a.vec_out = (reinterpret_cast<uintptr_t>(a.C) & 15) == 0 && (a.ldc * elt) % 16 == 0;
+  const dim3 grid(static_cast<unsigned>(plan_max_tiles(plan.pairs, plan.groups, b) * a.tiles_n));
+  hipLaunchKernelGGL(kern, grid, dim3(tile::kThreads), tile::kSmem, stream, a);
+  return hipGetLastError();
+}
+
+template <int OUT, bool GATED>
+hipError_t launch_grouped(const GroupedArgs& a, const RowPlan& plan, hipStream_t stream) {
+  if (plan.pairs / plan.groups < 64) return launch_stream<OUT, GATED>(a, plan, stream);
+  return a.K % tile::kSlice != 0 ? launch_tile_typed<OUT, GATED, true>(a, plan, stream)
+                                 : launch_tile_typed<OUT, GATED, false>(a, plan, stream);
+}
+
 }  // namespace
 
 hipError_t launch_linear_grouped(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* sa,
@@ -246,8 +280,8 @@ hipError_t launch_linear_grouped(const int8_t* A, int64_t lda, const int8_t* B, 
   a.C = C;
   a.ldc = ldc;
   if (out == Elt::F32)
-    return gated ? launch_stream<0, true>(a, plan, stream) : launch_stream<0, false>(a, plan, stream);
-  return gated ? launch_stream<1, true>(a, plan, stream) : launch_stream<1, false>(a, plan, stream);
+    return gated ? launch_grouped<0, true>(a, plan, stream) : launch_grouped<0, false>(a, plan, stream);
+  return gated ? launch_grouped<1, true>(a, plan, stream) : launch_grouped<1, false>(a, plan, stream);
 }
 
 }  // namespace convrot
