@@ -18,8 +18,10 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
+#include "device.h"
 #include "lanes.h"
 #include "launchers.h"
 
@@ -273,8 +275,13 @@ hipError_t launch_route_typed(const L* logits, int64_t ldl, int64_t M, int64_t E
 // by atomics, and pairs keep their order inside a group, so the plan is the
 // same on every run.  Inside a chunk wavefronts take turns: a lane's place is
 // the group's running count plus the lanes below it with the same id.
+//   Bound by latency: the starts of the groups and of their tiles in all
+// lists come from one scan (a run of consecutive groups per thread, six sums
+// at once), which costs two barriers instead of three per sum.
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kPlanSums = 1 + kPlanLists;  // pairs, and tiles of every list
 
 __device__ __forceinline__ int group_of(int32_t id, int E) { return id < 0 || id >= E ? E : id; }
 
@@ -289,35 +296,6 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(const int32_t*
   for (int i = threadIdx.x; i <= E; i += kPlanThreads) counts[static_cast<int64_t>(blockIdx.x) * (E + 1) + i] = hist[i];
 }
 
-// Exclusive scan of v[0 .. n) in LDS (v[n] receives the total); `part` holds
-// one value per wavefront.
-__device__ void scan_exclusive(int32_t* v, int n, int32_t* part) {
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  int carry = 0;
-  for (int base = 0; base < n; base += kPlanThreads) {
-    const int i = base + threadIdx.x;
-    const int x = i < n ? v[i] : 0;
-    int s = x;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(s, d);
-      if (lane >= d) s += o;
-    }
-    if (lane == 63) part[wid] = s;
-    __syncthreads();
-    int before = carry, all = carry;
-    for (int w = 0; w < kPlanThreads / 64; ++w) {
-      if (w < wid) before += part[w];
-      all += part[w];
-    }
-    if (i < n) v[i] = before + s - x;
-    carry = all;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) v[n] = carry;
-  __syncthreads();
-}
-
 // counts: the chunks' counts of plan_count_kernel, or NULL to count the ids.
 __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t* __restrict__ ids, int pairs, int E,
                                                                   int chunk, const int32_t* __restrict__ counts,
@@ -326,36 +304,84 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
                                                                   int32_t* __restrict__ tiles) {
   extern __shared__ int32_t lds[];
   const int bins = E + 1;
-  int32_t* start = lds;             // [E + 2]: all pairs per group, then where each group starts
-  int32_t* place = start + bins + 1;  // [E + 2]: pairs before this chunk, then this chunk's next place
-  int32_t* part = place + bins + 1;   // [16]
+  int32_t* place = lds;          // [bins]: pairs before this chunk, then this chunk's next place
+  int32_t* sums = place + bins;  // [kPlanSums][bins + 1]: sums[0] first the pairs per group
+  __shared__ int32_t part[kPlanSums][kPlanWaves];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
   const int c0 = blockIdx.x * chunk, c1 = min(pairs, c0 + chunk);
-  for (int i = tid; i < bins; i += kPlanThreads) start[i] = place[i] = 0;
+  for (int i = tid; i < bins; i += kPlanThreads) sums[i] = place[i] = 0;
   __syncthreads();
   if (counts == nullptr) {
     for (int i = tid; i < pairs; i += kPlanThreads) {
       const int g = group_of(ids[i], E);
-      atomicAdd(i < c0 ? &place[g] : &start[g], 1);
+      atomicAdd(&sums[g], 1);
+      if (i < c0) atomicAdd(&place[g], 1);
     }
-    __syncthreads();
-    for (int i = tid; i < bins; i += kPlanThreads) start[i] += place[i];
   } else {
-    // One value per group: integer sums, so the order does not matter.
-    const int chunks = gridDim.x;
-    for (int i = tid; i < bins * chunks; i += kPlanThreads) {
-      const int n = counts[i];
-      if (n == 0) continue;
+    // Every group's counts of all chunks and of those before this one; with
+    // few groups the threads share out the chunks too.
+    const int chunks = gridDim.x, me = blockIdx.x;
+    const int parts = max(1, kPlanThreads / bins);
+    for (int i = tid; i < bins * parts; i += kPlanThreads) {
       const int g = i % bins;
-      atomicAdd(&start[g], n);
-      if (i / bins < static_cast<int>(blockIdx.x)) atomicAdd(&place[g], n);
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int c = i / bins; c < chunks; c += parts) {
+        const int n = counts[static_cast<int64_t>(c) * bins + g];
+        all += n;
+        before += c < me ? n : 0;
+      }
+      atomicAdd(&sums[g], all);
+      atomicAdd(&place[g], before);
     }
   }
   __syncthreads();
-  scan_exclusive(start, bins, part);
-  for (int i = tid; i < bins; i += kPlanThreads) place[i] += start[i];
-  if (blockIdx.x == 0)
-    for (int i = tid; i <= E; i += kPlanThreads) offsets[i] = start[i];
+  // Exclusive scans over the groups: thread t owns groups t per .. + per - 1.
+  const int per = (bins + kPlanThreads - 1) / kPlanThreads;
+  int own[kPlanSums] = {};
+  for (int i = tid * per; i < min(bins, (tid + 1) * per); ++i) {
+    const int n = sums[i];
+    own[0] += n;
+#pragma unroll
+    for (int b = 0; b < kPlanLists; ++b) own[1 + b] += (n + (16 << b) - 1) >> (4 + b);
+  }
+  int upto[kPlanSums];
+#pragma unroll
+  for (int q = 0; q < kPlanSums; ++q) {
+    int s = own[q];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(s, d);
+      if (lane >= d) s += o;
+    }
+    upto[q] = s;
+    if (lane == 63) part[q][wid] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kPlanSums; ++q) {
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) before += w < wid ? part[q][w] : 0;
+    upto[q] += before - own[q];
+  }
+  for (int i = tid * per; i < min(bins, (tid + 1) * per); ++i) {
+    const int n = sums[i];
+    sums[i] = upto[0];
+    place[i] += upto[0];
+    if (blockIdx.x == 0 && i <= E) offsets[i] = upto[0];
+    upto[0] += n;
+#pragma unroll
+    for (int b = 0; b < kPlanLists; ++b) {
+      sums[(1 + b) * (bins + 1) + i] = upto[1 + b];
+      upto[1 + b] += (n + (16 << b) - 1) >> (4 + b);
+    }
+    if (i == E) {  // the totals
+      sums[bins] = upto[0];
+#pragma unroll
+      for (int b = 0; b < kPlanLists; ++b) sums[(1 + b) * (bins + 1) + bins] = upto[1 + b];
+    }
+  }
   __syncthreads();
 
   // This chunk's pairs, 64 per wavefront and turn.
@@ -370,7 +396,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
       same &= (g & b) != 0 ? set : ~set;
     }
     const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
-    const int turns = min(kPlanThreads / 64, (c1 - base + 63) / 64);
+    const int turns = min(kPlanWaves, (c1 - base + 63) / 64);
     for (int w = 0; w < turns; ++w) {
       if (w == wid && live) {
         const int p = place[g];
@@ -386,14 +412,10 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
   // many positions, the ungrouped positions (group E) last; entry {group,
   // first position}.  The lists are shared out over the workgroups.
   for (int b = 0; b < kPlanLists; ++b) {
-    const int bm = 16 << b;
-    __syncthreads();
-    for (int i = tid; i < bins; i += kPlanThreads) place[i] = (start[i + 1] - start[i] + bm - 1) / bm;
-    __syncthreads();
-    scan_exclusive(place, bins, part);
-    const int total = place[bins];
+    const int32_t* first = sums + (1 + b) * (bins + 1);
+    const int total = first[bins];
     if (blockIdx.x == 0 && tid == 0) {
-      tiles[b] = place[E];
+      tiles[b] = first[E];
       tiles[kPlanLists + b] = total;
     }
     int32_t* list = tiles + plan_list_at(pairs, E, b);
@@ -401,10 +423,10 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
       int lo = 0, hi = bins - 1;  // the last group that starts at or before tile t
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (place[mid] <= t) lo = mid; else hi = mid - 1;
+        if (first[mid] <= t) lo = mid; else hi = mid - 1;
       }
       list[2 * t] = lo;
-      list[2 * t + 1] = start[lo] + (t - place[lo]) * bm;
+      list[2 * t + 1] = sums[lo] + ((t - first[lo]) << (4 + b));
     }
   }
 }
@@ -493,11 +515,13 @@ hipError_t launch_route(const void* logits, Elt dt, int64_t ldl, int64_t M, int6
               : launch_route_typed<__bf16, false>(l, ldl, M, E, bias, ra, ids, weights, stream);
 }
 
-// Pairs counted by every workgroup anew, and pairs per chunk.
+// Pairs counted by every workgroup anew, and pairs per chunk.  A chunk's
+// turns are serial, and every workgroup reads all chunks' counts: 1024 pairs
+// (16 turns) where the counts are added, 256 where each workgroup counts.
 static constexpr int64_t kPlanRecount = 8192;
 static int64_t plan_chunk(int64_t pairs) {
   const int64_t c = (pairs + kPlanMaxChunks - 1) / kPlanMaxChunks;
-  return std::max<int64_t>(256, (c + 63) / 64 * 64);
+  return std::max<int64_t>(pairs > kPlanRecount ? 1024 : 256, (c + 63) / 64 * 64);
 }
 
 int64_t plan_ints(int64_t pairs, int64_t E) {
@@ -513,8 +537,15 @@ hipError_t launch_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32
   int32_t* counts = pairs > kPlanRecount ? tiles + plan_list_at(pairs, E, kPlanLists) : nullptr;
   if (counts != nullptr)
     hipLaunchKernelGGL(plan_count_kernel, grid, dim3(kPlanThreads), 4 * (E + 1), stream, ids, p, e, chunk, counts);
-  hipLaunchKernelGGL(plan_order_kernel, grid, dim3(kPlanThreads), 4 * (2 * (E + 2) + kPlanThreads / 64), stream, ids,
-                     p, e, chunk, counts, order, offsets, tiles);
+  const size_t lds = 4 * (E + 1 + kPlanSums * (E + 2));
+  if (lds > 65536 - 1024) {  // more than about 2300 groups
+    static std::atomic<uint64_t> lds_set{0};
+    const hipError_t err = set_lds_limit(reinterpret_cast<const void*>(plan_order_kernel),
+                                         4 * (kPlanMaxGroups + 1 + kPlanSums * (kPlanMaxGroups + 2)), lds_set);
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL(plan_order_kernel, grid, dim3(kPlanThreads), lds, stream, ids, p, e, chunk, counts, order,
+                     offsets, tiles);
   return hipGetLastError();
 }
 

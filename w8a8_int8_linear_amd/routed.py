@@ -24,6 +24,10 @@ import torch
 from . import _lib
 from .api import (GELU_ERF, GELU_TANH, Packed, _check_bias, _check_out, _DT, _ld, _need_cuda, _ptr, _stream, _ws)
 
+# The current stream's handle by device index, without building a Stream
+# object (a tenth of the time, for calls that take a few microseconds).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 SILU = "silu"
 _FN = {None: _lib.ACT_NONE, GELU_ERF: _lib.ACT_GELU_ERF, GELU_TANH: _lib.ACT_GELU_TANH, SILU: _lib.ACT_SILU}
 
@@ -52,6 +56,16 @@ def _need_float(t: torch.Tensor, name: str) -> None:
 def _dense(t: torch.Tensor, dtype: torch.dtype, shape, name: str) -> None:
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+
+
+def _call(device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) on the current stream of ``device``, with that device
+    current; raises on an error status."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            _lib.check(fn(*args, _stream(device)))
+    else:
+        _lib.check(fn(*args, _raw_stream(device.index) if _raw_stream is not None else _stream(device)))
 
 
 # ---------------------------------------------------------------------------
@@ -89,9 +103,8 @@ def route(logits: torch.Tensor, top_k: int, score: str = SOFTMAX, bias: torch.Te
     _need_device(weights, dev, "weights")
     rule = _lib.Routing(_SCORE[score], int(top_k), int(groups), int(top_groups), int(bool(renormalise)), float(scale))
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        _lib.check(lib.convrot_route(logits.data_ptr(), _DT[logits.dtype], _ld(logits), M, E, _ptr(bias),
-                                     ctypes.byref(rule), ids.data_ptr(), weights.data_ptr(), _stream(dev)))
+    _call(dev, lib.convrot_route, logits.data_ptr(), _DT[logits.dtype], _ld(logits), M, E, _ptr(bias),
+          ctypes.byref(rule), ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -99,12 +112,13 @@ def route(logits: torch.Tensor, top_k: int, score: str = SOFTMAX, bias: torch.Te
 # The plan
 # ---------------------------------------------------------------------------
 
-@dataclass
+@dataclass(frozen=True)
 class RowGroups:
     """The (row, choice) pairs of a batch in the order of their groups
     (convrot_row_groups).  Pair p belongs to row p // per_row; group g's
     pairs are ``order[offsets[g]:offsets[g + 1]]``, ascending, and pairs
-    without a group come last."""
+    without a group come last.  The buffers are fixed (``group_rows`` with
+    ``out`` rewrites their contents), so they are checked once."""
     order: torch.Tensor     # [pairs] int32
     offsets: torch.Tensor   # [groups + 1] int32
     tiles: torch.Tensor     # int32, the library's row tiles
@@ -116,6 +130,13 @@ class RowGroups:
         return self.order.shape[0]
 
     def descriptor(self) -> _lib.RowGroups:
+        desc = self.__dict__.get("_checked")
+        if desc is None:
+            desc = self._check()
+            object.__setattr__(self, "_checked", desc)
+        return desc
+
+    def _check(self) -> _lib.RowGroups:
         for t, name in ((self.order, "order"), (self.offsets, "offsets"), (self.tiles, "tiles")):
             if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 vector")
@@ -149,16 +170,14 @@ def group_rows(ids: torch.Tensor, groups: int, out: RowGroups | None = None) -> 
         raise ValueError("ids must hold at least one choice per row")
     pairs, dev = ids.numel(), ids.device
     if out is None:
-        out = RowGroups(torch.empty((pairs,), dtype=torch.int32, device=dev),
-                        torch.empty((groups + 1,), dtype=torch.int32, device=dev),
-                        torch.empty((row_groups_tiles(pairs, groups),), dtype=torch.int32, device=dev), groups, per_row)
+        sizes = [pairs, groups + 1, row_groups_tiles(pairs, groups)]
+        out = RowGroups(*torch.empty((sum(sizes),), dtype=torch.int32, device=dev).split(sizes), groups, per_row)
     elif (out.pairs, out.groups, out.per_row) != (pairs, groups, per_row):
         raise ValueError("out is a plan of other sizes")
     _need_device(out.order, dev, "out")
     desc = out.descriptor()
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        _lib.check(lib.convrot_group_rows(ids.data_ptr(), ctypes.byref(desc), _stream(dev)))
+    _call(dev, lib.convrot_group_rows, ids.data_ptr(), ctypes.byref(desc))
     return out
 
 
@@ -206,10 +225,8 @@ def linear_grouped(act_in: Packed, w: Packed, groups: RowGroups, bias: torch.Ten
     a, b, g = act_in.descriptor(), w.descriptor(), groups.descriptor()
     dev = act_in.q.device
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        _lib.check(lib.convrot_linear_grouped(ctypes.byref(a), ctypes.byref(b), _ptr(bias), _FN[act], ctypes.byref(g),
-                                              _ORDER[source], _ORDER[dest], out.data_ptr(), _DT[out.dtype], _ld(out),
-                                              _stream(dev)))
+    _call(dev, lib.convrot_linear_grouped, ctypes.byref(a), ctypes.byref(b), _ptr(bias), _FN[act], ctypes.byref(g),
+          _ORDER[source], _ORDER[dest], out.data_ptr(), _DT[out.dtype], _ld(out))
     return out
 
 
@@ -227,10 +244,8 @@ def linear_gated_grouped(act_in: Packed, w_gate: Packed, w_up: Packed, groups: R
     a, wg, wu, g = act_in.descriptor(), w_gate.descriptor(), w_up.descriptor(), groups.descriptor()
     dev = act_in.q.device
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        _lib.check(lib.convrot_linear_gated_grouped(
-            ctypes.byref(a), ctypes.byref(wg), _ptr(b_gate), ctypes.byref(wu), _ptr(b_up), _FN[act], ctypes.byref(g),
-            _ORDER[source], _ORDER[dest], out.data_ptr(), _DT[out.dtype], _ld(out), _stream(dev)))
+    _call(dev, lib.convrot_linear_gated_grouped, ctypes.byref(a), ctypes.byref(wg), _ptr(b_gate), ctypes.byref(wu),
+          _ptr(b_up), _FN[act], ctypes.byref(g), _ORDER[source], _ORDER[dest], out.data_ptr(), _DT[out.dtype], _ld(out))
     return out
 
 
@@ -256,9 +271,8 @@ def combine_rows(y: torch.Tensor, weights: torch.Tensor, ids: torch.Tensor, grou
         out = torch.empty((M, N), dtype=y.dtype, device=dev)
     _check_out(out, M, N, (y.dtype,), dev)
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        _lib.check(lib.convrot_combine_rows(y.data_ptr(), _DT[y.dtype], _ld(y), weights.data_ptr(), ids.data_ptr(), M, k,
-                                            N, int(groups), out.data_ptr(), _ld(out), _stream(dev)))
+    _call(dev, lib.convrot_combine_rows, y.data_ptr(), _DT[y.dtype], _ld(y), weights.data_ptr(), ids.data_ptr(), M, k, N,
+          int(groups), out.data_ptr(), _ld(out))
     return out
 
 
@@ -273,6 +287,13 @@ def lora_grouped_workspace_bytes(M: int, K: int, r: int, groups: int) -> int:
     out = ctypes.c_int64(0)
     _lib.check(lib.convrot_lora_grouped_workspace_bytes(M, K, r, groups, ctypes.byref(out)))
     return out.value
+
+
+def _lora_workspace(device: torch.device, M: int, K: int, r: int, groups: int) -> int:
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return max(lora_grouped_workspace_bytes(M, K, r, groups), 16)
+    return max(lora_grouped_workspace_bytes(M, K, r, groups), 16)
 
 
 def _need_stack(t: torch.Tensor, name: str) -> None:
@@ -323,12 +344,10 @@ def lora_add_grouped(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scales: 
     ldb, stride_b = _stack_strides(b)
     g = groups.descriptor()
     lib = _lib.load()
-    with torch.cuda.device(dev):
-        if workspace is None:
-            workspace = torch.empty((max(lora_grouped_workspace_bytes(M, K, r, E), 16),), dtype=torch.uint8, device=dev)
-        wp, wn = _ws(workspace, dev)
-        _lib.check(lib.convrot_lora_add_grouped(
-            x.data_ptr(), _ld(x), M, K, a.data_ptr(), lda, stride_a, b.data_ptr(), ldb, stride_b, N, r,
-            scales.data_ptr(), ctypes.byref(g), y.data_ptr(), _ld(y), _DT[y.dtype], out.data_ptr(), _ld(out), wp, wn,
-            _stream(dev)))
+    if workspace is None:
+        workspace = torch.empty((_lora_workspace(dev, M, K, r, E),), dtype=torch.uint8, device=dev)
+    wp, wn = _ws(workspace, dev)
+    _call(dev, lib.convrot_lora_add_grouped, x.data_ptr(), _ld(x), M, K, a.data_ptr(), lda, stride_a, b.data_ptr(), ldb,
+          stride_b, N, r, scales.data_ptr(), ctypes.byref(g), y.data_ptr(), _ld(y), _DT[y.dtype], out.data_ptr(),
+          _ld(out), wp, wn)
     return out
