@@ -106,13 +106,20 @@ def test_group_rows(cuda, M, k, E):
         p = cr.group_rows(to_dev(ids, torch.int32), E)
         order, offsets = R.plan(ids, E)
         assert np.array_equal(to_np(p.order), order) and np.array_equal(to_np(p.offsets), offsets), kind
-        # the row tiles: every group cut from its start, in order, the rest last
+        # the row tiles: every group cut evenly (in whole 16 rows) into as few
+        # as hold it, in order, the rest last
         t = to_np(p.tiles)
         starts = np.append(offsets, M * k)
         at = 10
         for b in range(5):
             bm = 16 << b
-            want = [(e, q) for e in range(E + 1) for q in range(starts[e], starts[e + 1], bm)]
+            want = []
+            for e in range(E + 1):
+                rows = int(starts[e + 1] - starts[e])
+                n = -(-rows // bm)
+                step = bm if n <= 1 else (-(-rows // n) + 15) // 16 * 16
+                want += [(e, int(starts[e]) + i * step) for i in range(n)]
+                assert n <= 1 or (n - 1) * step < rows <= n * step <= n * bm
             assert t[b] == sum(e < E for e, _ in want) and t[5 + b] == len(want), (kind, bm)
             assert np.array_equal(t[at:at + 2 * len(want)].reshape(-1, 2), np.array(want, dtype=np.int32).reshape(-1, 2))
             at += 2 * (M * k // bm + min(E + 1, M * k))
@@ -149,8 +156,12 @@ def _ids(M, k, E, seed, unused=0.0):
     return ids.reshape(M, k)
 
 
-# M, k, E, K, N, G, share of pairs without a group
-PRODUCTS = [(1, 1, 1, 16, 1, 16, 0), (1, 8, 128, 256, 96, 256, 0), (2, 2, 8, 1152, 100, 64, 0), (16, 2, 8, 1152, 260, 64, 0.2),
+# M, k, E, K, N, G, share of pairs without a group: every kernel the launch
+# rules choose (few and many workgroups of the ring's three tile heights, the
+# tiled kernel), whole and ragged K and N
+PRODUCTS = [(20, 2, 16, 208, 4200, 16, 0.1), (20, 2, 16, 384, 4224, 64, 0), (160, 1, 16, 128, 1350, 64, 0.1),
+            (200, 1, 4, 96, 5200, 16, 0.05), (210, 1, 4, 256, 5185, 64, 0.05),
+            (1, 1, 1, 16, 1, 16, 0), (1, 8, 128, 256, 96, 256, 0), (2, 2, 8, 1152, 100, 64, 0), (16, 2, 8, 1152, 260, 64, 0.2),
             (5, 3, 4, 48, 33, 16, 0.5), (40, 4, 6, 2048, 130, 256, 0.1), (150, 2, 3, 320, 77, 64, 0.1),
             (300, 1, 2, 1040, 200, 16, 0.0), (513, 2, 4, 1152, 300, 64, 0.05), (7, 2, 300, 256, 40, 64, 0.3),
             (700, 2, 3, 256, 513, 64, 0.0), (1300, 1, 2, 208, 272, 16, 0.1)]

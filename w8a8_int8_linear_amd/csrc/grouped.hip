@@ -10,244 +10,69 @@
 // rows carry the bits that convrot_linear (_act, _gated) gives for its weight
 // alone.
 //
-// Streaming kernel.  A workgroup takes one tile of the plan (up to 16 MT
-// positions of one group) and 16 output features; its waves split K into
-// runs of 64-byte steps (v_mfma_i32_16x16x64_i8, weights as the row operand)
-// straight from memory into registers, add their partial sums through LDS and
-// finish 16 positions per wave.  Bound by the weights' bytes where groups
-// hold few rows; every group's weight is read once per tile.
-#include <hip/hip_runtime.h>
-
-#include <algorithm>
-#include <atomic>
-#include <type_traits>
-
-#include "device.h"
-#include "epilogue.h"
-#include "launchers.h"
+// Few rows per group: the weight-streaming ring (grouped_ring.h), bound by the
+// weights' bytes.  Many: the tiled kernel (grouped_tile.h).
+#include "grouped.h"
+#include "grouped_ring.h"
 
 namespace convrot {
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-
-struct GroupedArgs {
-  const uint8_t* A;
-  int64_t lda;
-  const float* sa;
-  const uint8_t* B;
-  int64_t ldb;
-  const float* sb;
-  const float* bias;
-  const uint8_t* B2;
-  int64_t ldb2;
-  const float* sb2;
-  const float* bias2;
-  const int32_t* order;
-  const int32_t* offsets;
-  const int32_t* list;   // tiles of the plan, {group, first position}
-  const int32_t* count;  // how many of them
-  int per_row;
-  int source;  // RowOrder of A's rows
-  int dest;    // RowOrder of C's rows
-  int act;
-  int N;
-  int K;
-  void* C;
-  int64_t ldc;
-  int tiles_n;   // feature blocks
-  bool vec_out;  // rows of C take 16-byte stores
-};
-
-// SiLU, y / (1 + e^{-y}), with the hardware exp2 and reciprocal (at
-// 2^.. = inf the reciprocal is 0).
-__device__ __forceinline__ float silu(float y) {
-  return y * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y * -1.4426950408889634f));
-}
-
-__device__ __forceinline__ float apply_act(int act, float y) {
-  switch (act) {  // uniform
-    case 1: return activation<1>(y);
-    case 2: return activation<2>(y);
-    case 3: return silu(y);
-    default: return y;
-  }
-}
-
-__device__ __forceinline__ int64_t row_of(int order, int pos, int pair, int per_row) {
-  return order == static_cast<int>(RowOrder::Sorted) ? pos
-         : order == static_cast<int>(RowOrder::Pair) ? pair
-                                                     : pair / per_row;
-}
-
-template <typename T>
-__device__ __forceinline__ bool aligned4(const T* p) {
-  return (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0;
-}
-
-// Four consecutive features of one output row, the columns past N dropped.
-template <int OUT>
-__device__ __forceinline__ void store4(void* C, int64_t at, int n, int N, const float y[4]) {
-  if constexpr (OUT == 0) {
-    float* out = static_cast<float*>(C) + at + n;
-    if (n + 3 < N && aligned4(out)) {
-      *reinterpret_cast<f32x4*>(out) = f32x4{y[0], y[1], y[2], y[3]};
-    } else {
-      for (int r = 0; r < 4 && n + r < N; ++r) out[r] = y[r];
-    }
-  } else {
-    __bf16* out = static_cast<__bf16*>(C) + at + n;
-    if (n + 3 < N && aligned4(out)) {
-      *reinterpret_cast<bf16x4*>(out) = bf16x4{static_cast<__bf16>(y[0]), static_cast<__bf16>(y[1]),
-                                               static_cast<__bf16>(y[2]), static_cast<__bf16>(y[3])};
-    } else {
-      for (int r = 0; r < 4 && n + r < N; ++r) out[r] = static_cast<__bf16>(y[r]);
-    }
-  }
-}
-
-}  // namespace
-}  // namespace convrot
-
-#include "grouped_tile.h"
-
-namespace convrot {
-namespace {
-
-template <int OUT, bool GATED, int MT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void grouped_stream_kernel(GroupedArgs a) {
-  constexpr int kW = GATED ? 2 : 1;
-  constexpr int kAhead = 4;  // K steps in flight
-  static_assert(MT <= WAVES, "one wave finishes each 16 positions");
-  __shared__ i32x4 partial[WAVES][kW][MT][64];
-  const int tile = blockIdx.x / a.tiles_n;
-  if (tile >= *a.count) return;
-  const int n0 = (blockIdx.x % a.tiles_n) * 16;
-  const int group = a.list[2 * tile], p0 = a.list[2 * tile + 1];
-  const int cnt = min(16 * MT, a.offsets[group + 1] - p0);
-  const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
-  const int row = lane & 15, ch = lane >> 4;
-
-  // Rows past the tile's last re-read it; features past the last likewise.
-  // Their results are dropped.
-  const uint8_t* x[MT];
-  int pos[MT], pair[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    pos[t] = p0 + min(16 * t + row, cnt - 1);
-    pair[t] = a.order[pos[t]];
-    x[t] = a.A + row_of(a.source, pos[t], pair[t], a.per_row) * a.lda + 16 * ch;
-  }
-  const int64_t wrow = static_cast<int64_t>(group) * a.N + min(n0 + row, a.N - 1);
-  const uint8_t* w[kW];
-  w[0] = a.B + wrow * a.ldb + 16 * ch;
-  if constexpr (GATED) w[1] = a.B2 + wrow * a.ldb2 + 16 * ch;
-
-  const int steps = (a.K + 63) / 64;
-  const int per = (steps + WAVES - 1) / WAVES;
-  const int s0 = wid * per, s1 = min(steps, s0 + per);
-  i32x4 acc[kW][MT] = {};
-  for (int s = s0; s < s1; s += kAhead) {
-    i32x4 fw[kAhead][kW], fx[kAhead][MT];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const bool live = s + u < s1 && 64 * (s + u) + 16 * ch < a.K;
-      const int64_t k = 64 * static_cast<int64_t>(s + u);
-#pragma unroll
-      for (int j = 0; j < kW; ++j) fw[u][j] = live ? *reinterpret_cast<const i32x4*>(w[j] + k) : i32x4{};
-#pragma unroll
-      for (int t = 0; t < MT; ++t) fx[u][t] = live ? *reinterpret_cast<const i32x4*>(x[t] + k) : i32x4{};
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < kW; ++j)
-          acc[j][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[u][j], fx[u][t], acc[j][t], 0, 0, 0);
-  }
-#pragma unroll
-  for (int j = 0; j < kW; ++j)
-#pragma unroll
-    for (int t = 0; t < MT; ++t) partial[wid][j][t][lane] = acc[j][t];
-  __syncthreads();
-  // Lane holds position 16 t + row and features n0 + 4 ch + r.
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    if (wid != t || 16 * t + row >= cnt) continue;
-    const float sr = a.sa[row_of(a.source, pos[t], pair[t], a.per_row)];
-    const int64_t out = row_of(a.dest, pos[t], pair[t], a.per_row) * a.ldc;
-    i32x4 sum[kW];
-#pragma unroll
-    for (int j = 0; j < kW; ++j) {
-      sum[j] = partial[0][j][t][lane];
-#pragma unroll
-      for (int v = 1; v < WAVES; ++v) sum[j] += partial[v][j][t][lane];
-    }
-    float y[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t col = static_cast<int64_t>(group) * a.N + min(n0 + 4 * ch + r, a.N - 1);
-      const float z = fmaf(static_cast<float>(sum[0][r]), sr * a.sb[col], a.bias != nullptr ? a.bias[col] : 0.f);
-      y[r] = apply_act(a.act, z);
-      if constexpr (GATED)
-        y[r] *= fmaf(static_cast<float>(sum[1][r]), sr * a.sb2[col], a.bias2 != nullptr ? a.bias2[col] : 0.f);
-    }
-    store4<OUT>(a.C, out, n0 + 4 * ch, a.N, y);
-  }
-}
-
-template <int OUT, bool GATED>
-hipError_t launch_stream(GroupedArgs a, const RowPlan& plan, hipStream_t stream) {
-  // Tiles of 16 positions, or of more where groups hold more on average, so
-  // that a group's weight is read by few workgroups.
-  const int64_t avg = plan.pairs / plan.groups;
-  const int b = avg <= 16 ? 0 : avg <= 32 ? 1 : 2;
-  a.list = plan.tiles + plan_list_at(plan.pairs, plan.groups, b);
-  a.count = plan.tiles + b;
-  a.tiles_n = (a.N + 15) / 16;
-  const dim3 grid(static_cast<unsigned>(plan_max_tiles(plan.pairs, plan.groups, b) * a.tiles_n));
-  // Eight waves where each still gets two K steps.
-  const bool wide = a.K >= 1024;
-#define CONVROT_GROUPED(MT_)                                                                              \
-  if (wide)                                                                                               \
-    hipLaunchKernelGGL((grouped_stream_kernel<OUT, GATED, MT_, 8>), grid, dim3(512), 0, stream, a);       \
-  else                                                                                                    \
-    hipLaunchKernelGGL((grouped_stream_kernel<OUT, GATED, MT_, 4>), grid, dim3(256), 0, stream, a)
-  switch (b) {
-    case 0: CONVROT_GROUPED(1); break;
-    case 1: CONVROT_GROUPED(2); break;
-    default: CONVROT_GROUPED(4); break;
-  }
-#undef CONVROT_GROUPED
-  return hipGetLastError();
-}
-
-template <int OUT, bool GATED, bool KTAIL>
-hipError_t launch_tile_typed(GroupedArgs a, const RowPlan& plan, hipStream_t stream) {
-  auto kern = tile::grouped_tile_kernel<OUT, GATED, KTAIL>;
+template <int OUT, bool GATED, bool KTAIL, int MT, int NW, bool SPLIT>
+hipError_t launch_ring_typed(GroupedArgs a, const RowPlan& plan, hipStream_t stream) {
+  auto kern = ring::grouped_ring_kernel<OUT, GATED, KTAIL, MT, NW, SPLIT>;
+  constexpr int kSmem = ring::smem_bytes<MT, NW, SPLIT>();
   static std::atomic<uint64_t> lds_set{0};
-  const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), tile::kSmem, lds_set);
+  const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), kSmem, lds_set);
   if (e != hipSuccess) return e;
-  constexpr int b = 4;  // tiles of 256 positions
+  constexpr int b = MT == 1 ? 0 : MT == 2 ? 1 : 2;
   a.list = plan.tiles + plan_list_at(plan.pairs, plan.groups, b);
   a.count = plan.tiles + b;
-  constexpr int kFeat = GATED ? tile::kRows / 2 : tile::kRows;
+  constexpr int kFeat = (GATED ? 16 : 32) * (SPLIT ? 1 : NW);
   a.tiles_n = (a.N + kFeat - 1) / kFeat;
-  const int elt = OUT == 0 ? 4 : 2;
-  a.vec_out = (reinterpret_cast<uintptr_t>(a.C) & 15) == 0 && (a.ldc * elt) % 16 == 0;
   const dim3 grid(static_cast<unsigned>(plan_max_tiles(plan.pairs, plan.groups, b) * a.tiles_n));
-  hipLaunchKernelGGL(kern, grid, dim3(tile::kThreads), tile::kSmem, stream, a);
+  hipLaunchKernelGGL(kern, grid, dim3(64 * NW), kSmem, stream, a);
   return hipGetLastError();
+}
+
+// The kernel for a launch, by what the host knows of the groups: the number of
+// pairs and groups (rows per group on average).  Measured on one box, 8 to 32
+// groups, K = 1024 to 6912 (us, the ring alone against the other side):
+//   rows per tile of the ring, by rows per group:
+//     4 rows   16: 14.0, 32: 14.6, 64: 15.6       8 rows  16: 17.8, 32: 15.9, 64: 16.9
+//     32 rows  16: 24.8, 32: 21.4, 64: 23.2       64 rows 16: 34.8, 32: 28.0, 64: 26.1
+//   tiled kernel against the ring's 64-row tiles:
+//     128 rows 39.7 / 34.6 and 54.7 / 53.7        256 rows 54.3 / 52.7 and 68.5 / 80.0
+//   K shared by the workgroup's waves (2, 4), with fewer workgroups than CUs:
+//     72 workgroups 25.6, 17.9 (2), 16.6 (4)      128: 10.9, 9.3, 9.0
+//     256: 15.1, 13.8, 15.5                       512: 26.6, 26.8, 27.8
+template <int OUT, bool GATED, bool KTAIL>
+hipError_t launch_ring(const GroupedArgs& a, const RowPlan& plan, hipStream_t stream) {
+  constexpr int kNW = 4;
+  const int64_t avg = plan.pairs / plan.groups;
+  const int64_t blocks = (a.N + (GATED ? 16 : 32) * kNW - 1) / ((GATED ? 16 : 32) * kNW);
+  // workgroups of a launch with tiles of 16 << b rows
+  auto workgroups = [&](int b) {
+    return blocks * std::max<int64_t>(std::min<int64_t>(plan.groups, plan.pairs), plan.pairs >> (4 + b));
+  };
+  if (avg > 40 && workgroups(2) >= 160) return launch_ring_typed<OUT, GATED, KTAIL, 4, kNW, false>(a, plan, stream);
+  if (avg >= 6)
+    return workgroups(1) >= 160 ? launch_ring_typed<OUT, GATED, KTAIL, 2, kNW, false>(a, plan, stream)
+                                : launch_ring_typed<OUT, GATED, KTAIL, 2, 2, true>(a, plan, stream);
+  const int64_t w = workgroups(0);
+  return w >= 512   ? launch_ring_typed<OUT, GATED, KTAIL, 1, kNW, false>(a, plan, stream)
+         : w >= 160 ? launch_ring_typed<OUT, GATED, KTAIL, 1, 2, true>(a, plan, stream)
+                    : launch_ring_typed<OUT, GATED, KTAIL, 1, 4, true>(a, plan, stream);
 }
 
 template <int OUT, bool GATED>
 hipError_t launch_grouped(const GroupedArgs& a, const RowPlan& plan, hipStream_t stream) {
-  if (plan.pairs / plan.groups < 64) return launch_stream<OUT, GATED>(a, plan, stream);
-  return a.K % tile::kSlice != 0 ? launch_tile_typed<OUT, GATED, true>(a, plan, stream)
-                                 : launch_tile_typed<OUT, GATED, false>(a, plan, stream);
+  if (plan.pairs / plan.groups >= 192) {
+    const Elt out = OUT == 0 ? Elt::F32 : Elt::BF16;
+    return GATED ? launch_grouped_tile_gated(a, plan, out, stream) : launch_grouped_tile(a, plan, out, stream);
+  }
+  return a.K % ring::kSlice != 0 ? launch_ring<OUT, GATED, true>(a, plan, stream)
+                                 : launch_ring<OUT, GATED, false>(a, plan, stream);
 }
 
 }  // namespace
@@ -272,6 +97,7 @@ hipError_t launch_linear_grouped(const int8_t* A, int64_t lda, const int8_t* B, 
   a.bias2 = bias2;
   a.order = plan.order;
   a.offsets = plan.offsets;
+  a.pairs = static_cast<int>(plan.pairs);
   a.per_row = plan.per_row;
   a.source = static_cast<int>(source);
   a.dest = static_cast<int>(dest);

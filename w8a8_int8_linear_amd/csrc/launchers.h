@@ -192,8 +192,8 @@ hipError_t launch_route(const void* logits, Elt dt, int64_t ldl, int64_t M, int6
                         RouteArgs ra, int32_t* ids, float* weights, hipStream_t stream);
 
 // The plan of pairs grouped by id.  `tiles` starts with kPlanLists counts of
-// grouped tiles and kPlanLists counts of all tiles, then list b (tiles of
-// 16 << b positions, {group, first position} each) at plan_list_at(.., b);
+// grouped tiles and kPlanLists counts of all tiles, then list b (tiles of at
+// most 16 << b positions, {group, first position} each) at plan_list_at(.., b);
 // the ungrouped positions are group E.
 constexpr int kPlanLists = 5;
 constexpr int64_t kPlanMaxChunks = 256;
@@ -208,6 +208,13 @@ __host__ __device__ inline int64_t plan_list_at(int64_t pairs, int64_t E, int b)
   int64_t at = 2 * kPlanLists;
   for (int i = 0; i < b; ++i) at += 2 * plan_max_tiles(pairs, E, i);
   return at;
+}
+// Rows of a group's tiles in the list of 16 << b: the group is cut evenly into
+// as few tiles as it needs (in whole 16 rows; the last may be shorter), so
+// that their work differs little.
+__host__ __device__ inline int plan_tile_rows(int rows, int b) {
+  const int n = (rows + (16 << b) - 1) >> (4 + b);
+  return n <= 1 ? 16 << b : ((rows + n - 1) / n + 15) & ~15;
 }
 int64_t plan_ints(int64_t pairs, int64_t E);  // int32 values of `tiles`
 hipError_t launch_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32_t* order, int32_t* offsets,

@@ -77,7 +77,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void lora_grouped_down_kernel(Lora
   const int c0 = blockIdx.x % a.rb * kDownCols;
   if (tile >= *a.count) return;
   const int group = a.list[2 * tile], p0 = a.list[2 * tile + 1];
-  const int cnt = min(16 * MT, a.offsets[group + 1] - p0);
+  const int first = a.offsets[group], last = a.offsets[group + 1];
+  const int cnt = min(plan_tile_rows(last - first, MT == 4 ? 2 : 0), last - p0);
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int row = lane & 15, ch = lane >> 4;
   const int steps = (a.K + 31) / 32;
@@ -157,7 +158,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
   const int lane = threadIdx.x & 63, wid = threadIdx.x >> 6;
   const int row = lane & 15, ch = lane >> 4;
   const int sub = wid % MT;
-  const int end = group < a.groups ? a.offsets[group + 1] : a.M;
+  const int begin = a.offsets[group], last = group < a.groups ? a.offsets[group + 1] : a.M;
+  const int end = min(last, p0 + plan_tile_rows(last - begin, MT == 4 ? 2 : 0));
   const int cnt = min(16, end - p0 - 16 * sub);
   if (cnt <= 0 || (group == a.groups && !a.copy)) return;
   const int pos = p0 + 16 * sub + min(row, cnt - 1);

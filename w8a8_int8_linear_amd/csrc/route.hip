@@ -408,8 +408,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
     }
   }
 
-  // Tile lists: for rows-per-tile 16 << b, every group cut into tiles of that
-  // many positions, the ungrouped positions (group E) last; entry {group,
+  // Tile lists: for rows-per-tile 16 << b, every group cut evenly into as few
+  // tiles as hold it, the ungrouped positions (group E) last; entry {group,
   // first position}.  The lists are shared out over the workgroups.
   for (int b = 0; b < kPlanLists; ++b) {
     const int32_t* first = sums + (1 + b) * (bins + 1);
@@ -426,7 +426,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
         if (first[mid] <= t) lo = mid; else hi = mid - 1;
       }
       list[2 * t] = lo;
-      list[2 * t + 1] = sums[lo] + ((t - first[lo]) << (4 + b));
+      list[2 * t + 1] = sums[lo] + (t - first[lo]) * plan_tile_rows(sums[lo + 1] - sums[lo], b);
     }
   }
 }
