@@ -590,8 +590,9 @@ typedef struct {
  * experts are left, the remaining ids are -1 and their weights 0; a sum of
  * zero leaves zero weights.  A logit of +inf counts as the largest finite
  * value.
- * Without a bias and with one group the choice compares the logits
- * themselves; otherwise scores and choice values are computed in fp64.
+ * Without a bias experts are compared by their logits, exactly (the score is
+ * monotone in the logit).  Choice values with a bias, and group values, are
+ * compared as fp64 values.
  *   logits   [M, ldl] of ldt (CONVROT_F32 or CONVROT_BF16), element aligned,
  *            E columns, 1 <= E <= 1024
  *   bias     [E] fp32 or NULL

@@ -24,7 +24,6 @@ def route(logits, k, score, bias=None, groups=1, top_groups=1, renormalise=True,
     per = E // groups
     ids = np.full((M, k), -1, dtype=np.int32)
     weights = np.zeros((M, k))
-    wide = bias is not None or groups > 1
     for m in range(M):
         open_ = [i for i in range(E) if not np.isnan(x[m, i]) and x[m, i] != -np.inf]
         if score == "softmax":
@@ -44,14 +43,21 @@ def route(logits, k, score, bias=None, groups=1, top_groups=1, renormalise=True,
                     value[g] = sum(v)
             kept = sorted(value, key=lambda g: (-value[g], g))[:top_groups]
             open_ = [i for i in open_ if i // per in kept]
-        # the score is monotone in the logit: without a bias and groups the logits decide
-        rank = (lambda i: (-c[i], i)) if wide else (lambda i: (-x[m, i], i))
+        # the score is monotone in the logit: without a bias the logits decide
+        rank = (lambda i: (-c[i], i)) if bias is not None else (lambda i: (-x[m, i], i))
         for j, i in enumerate(sorted(open_, key=rank)[:k]):
             ids[m, j], weights[m, j] = i, s[i]
         if renormalise:
             t = weights[m].sum()
             weights[m] = weights[m] / t if t > 0 else 0.0
     return ids, weights * scale
+
+
+def choice_values(x, score, bias):
+    """fp64 choice values of one row of finite logits."""
+    x = np.asarray(x, dtype=np.float64)
+    s = np.exp(x - x.max()) / np.exp(x - x.max()).sum() if score == "softmax" else 1 / (1 + np.exp(-x))
+    return s if bias is None else s + np.asarray(bias, dtype=np.float64)
 
 
 def plan(ids, E):

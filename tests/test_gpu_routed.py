@@ -81,6 +81,30 @@ def test_route_ties_and_extremes(cuda):
                 assert np.all(np.abs(to_np(w) - w_ref) <= 64 * R.U * np.abs(w_ref)), (score, bias, groups)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top", [(64, 8, 1, 1), (256, 8, 8, 3), (500, 20, 4, 2), (1024, 40, 16, 5)])
+def test_route_near_ties(cuda, score, E, k, groups, top):
+    """Values that fp32 does not tell apart: logits a few units apart around
+    few levels, and a bias that undoes most of their differences (its own
+    rounding leaves some).  The choice is that of the fp64 values."""
+    g = np.random.default_rng(E)
+    M = 60
+    x = (g.integers(0, 4, (M, E)) * 0.5).astype(np.float32)
+    x = (x * (1 + g.integers(-3, 4, (M, E)) * 2.0 ** -23)).astype(np.float32)
+    for bias in (None, np.zeros(E, np.float32), (g.integers(0, 3, E) * 2.0 ** -24).astype(np.float32)):
+        ids, w = cr.route(to_dev(x, torch.float32), k, score=score, groups=groups, top_groups=top,
+                          bias=None if bias is None else to_dev(bias, torch.float32), renormalise=False)
+        ids_ref, w_ref = R.route(x, k, score, bias, groups, top, False)
+        ids = to_np(ids)
+        # equal up to choices whose fp64 values differ by less than their own rounding
+        for m in range(M):
+            if not np.array_equal(ids[m], ids_ref[m]):
+                assert bias is not None or groups > 1
+                c = R.choice_values(x[m], score, bias)
+                assert np.allclose(np.sort(c[ids[m]]), np.sort(c[ids_ref[m]]), rtol=0, atol=4e-16), m
+        assert np.all(np.abs(to_np(w) - w_ref) <= (64 + E + 16) * R.U * np.abs(w_ref) + 4e-7 * (groups > 1))
+
+
 def test_route_strided_logits_and_given_outputs(cuda):
     x = _logits(21, 40, 3, "f32")
     buf = torch.full((21, 53), 9.0, device=cuda)

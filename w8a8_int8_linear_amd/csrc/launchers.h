@@ -174,7 +174,7 @@ hipError_t launch_gemv_w4_gated(const int8_t* A, int64_t lda, const uint8_t* Bg,
 // Rows that choose their weights
 // ---------------------------------------------------------------------------
 
-// The router's rule (convrot_routing); per_group and log2_lanes are set by
+// The router's rule (convrot_routing); vec, vec_bias and lds_doubles are set by
 // the launcher.
 struct RouteArgs {
   int k;
@@ -183,8 +183,9 @@ struct RouteArgs {
   bool sigmoid;
   bool renormalise;
   float scale;
-  int per_group;   // experts per group
-  int log2_lanes;  // log2 of the lanes that share a group's value
+  bool vec;         // runs of logits are loaded as vectors
+  bool vec_bias;    // and runs of the bias
+  int lds_doubles;  // LDS of a wavefront for choice values
 };
 constexpr int64_t kRouteMaxExperts = 1024;
 constexpr int64_t kRouteMaxChoices = 64;  // one lane keeps each choice

@@ -3,18 +3,24 @@
 // sum that undoes the routing, for gfx950.
 //
 // Choice (convrot_route).  For a row of E logits l, scores
-//   s_i = e^{l_i - max l} / sum_j e^{l_j - max l}   or   1 / (1 + e^{-l_i}),
+//   s_i = e^{l_i - max l} / sum_j e^{l_j - max l}   or   1 / (1 + e^{-l_i})
 // choice values c_i = s_i + b_i, the values of groups of experts (the sum of
 // the two largest c), and the k largest c among the groups kept, ties to the
-// lowest index.  One wavefront takes a row, E / 64 consecutive experts per
-// lane, so that among equal values the lowest lane holds the lowest index and
-// a maximum over the wavefront needs no index beside it: the owner is the
-// first lane of a ballot.  Values are compared as unsigned keys whose order is
-// that of the numbers; key 0 is an expert that cannot be chosen.
-//   Without a bias and groups the score is a monotone function of the logit,
-// and the choice is made on the fp32 logits themselves, exactly.  Otherwise
-// two values of c may differ by less than fp32 resolves, so scores and choice
-// are computed in fp64.
+// lowest index.  Values are compared as unsigned keys whose order is that of
+// the numbers; key 0 is an expert that cannot be chosen.
+//   Without a bias the score is a monotone function of the logit, and experts
+// are compared by their fp32 logits, exactly.  A bias and group values need c
+// itself, and two of them may differ by less than fp32 resolves: they are
+// computed in fp32 with a bound on their error, and where two values
+// that the choice has to tell apart lie closer than their errors, the chosen
+// ones are ordered again in fp64, or the whole row is done again.
+//   Bound by a row's chain of dependent steps, not bytes (8192 rows of 256
+// fp32 logits are 8 MB, 1.5 us): 16 lanes take a row where its k allows (four
+// rows per wavefront), so that a maximum costs four lane exchanges for four
+// rows.  For those rows (k = 8, logistic, 8 groups, bias) fp64 throughout with
+// a wavefront per row took 23 us; this takes 13 us, and up to 20 us when a
+// row has to be done again, which is every other launch of that size.  Without
+// bias and groups: 6.4 us; one row of 128: 3.6 us.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -28,7 +34,7 @@
 namespace convrot {
 namespace {
 
-constexpr int kRouteRows = 4;  // rows (wavefronts) per workgroup
+constexpr int kRouteWaves = 4;  // wavefronts per workgroup
 
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.f);  // -0 and 0 are equal
@@ -37,6 +43,11 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __device__ __forceinline__ uint64_t order_key(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
   return (b >> 63) != 0 ? ~b : b | 0x8000000000000000ull;
+}
+
+// The fp32 value of a key.
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __builtin_bit_cast(float, (k >> 31) != 0 ? k & 0x7FFFFFFFu : ~k);
 }
 
 // x of the lane DPP control CTRL names (lanes outside ROW_MASK keep x).
@@ -86,128 +97,98 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// +inf counts as the largest finite value (the maximum's exponential is 1); a
+// NaN stays one.
+__device__ __forceinline__ float clamp_logit(float x) { return x > 3.402823466e38f ? 3.402823466e38f : x; }
 template <typename T>
 __device__ __forceinline__ float load_logit(const T* p) {
-  // +inf counts as the largest finite value (the maximum's exponential is
-  // 1); a NaN stays one
-  const float x = static_cast<float>(*p);
-  return x > 3.402823466e38f ? 3.402823466e38f : x;
+  return clamp_logit(static_cast<float>(*p));
 }
 
 // A logit an expert can be chosen by (-inf and NaN mark experts that cannot).
 __device__ __forceinline__ bool open_logit(float x) { return x >= -3.402823466e38f; }
 
-// Scores of a chosen expert in the precision T of the choice.
-template <typename T>
-__device__ __forceinline__ T score_of(float x, bool sigmoid, float mx, T inv_sum) {
-  if (sigmoid) return T(1) / (T(1) + exp(-static_cast<T>(x)));
-  return exp(static_cast<T>(x) - static_cast<T>(mx)) * inv_sum;
-}
-
-// NE: consecutive experts per lane.  WIDE: choice in fp64 with bias and
-// groups; otherwise on the logits.
-template <typename L, int NE, bool WIDE>
-__global__ __launch_bounds__(64 * kRouteRows) void route_kernel(const L* __restrict__ logits, int64_t ldl, int M,
-                                                                int E, const float* __restrict__ bias, RouteArgs ra,
-                                                                int32_t* __restrict__ ids,
-                                                                float* __restrict__ weights) {
-  using T = typename std::conditional<WIDE, double, float>::type;
-  using Key = typename std::conditional<WIDE, uint64_t, uint32_t>::type;
-  extern __shared__ __attribute__((aligned(16))) double choice_values[];  // [kRouteRows][E], with groups
+// One row in fp64 with a whole wavefront: E / 64 (rounded up, NE) consecutive
+// experts per lane, so that among equal values the lowest lane holds the
+// lowest index.  choice: E doubles of LDS of the wavefront's own (groups > 1).
+template <int NE, typename L>
+__device__ void route_row_exact(const L* row, int E, const float* bias, const RouteArgs& ra, double* choice,
+                                int32_t* ids, float* weights) {
   const int lane = threadIdx.x & 63;
-  const int wid = threadIdx.x >> 6;
-  const int m = blockIdx.x * kRouteRows + wid;
-  if (m >= M) return;  // (nothing below synchronises the workgroup)
-  const L* row = logits + static_cast<int64_t>(m) * ldl;
-
+  auto score = [&](float x, float mx, double inv_sum) {
+    if (ra.sigmoid) return 1.0 / (1.0 + exp(-static_cast<double>(x)));
+    return exp(static_cast<double>(x) - static_cast<double>(mx)) * inv_sum;
+  };
   float x[NE];
   bool open[NE];
+  uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
     const int i = lane * NE + j;
     x[j] = i < E ? load_logit(row + i) : 0.f;
-  }
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < NE; ++j) {
-    open[j] = lane * NE + j < E && open_logit(x[j]);
+    open[j] = i < E && open_logit(x[j]);
     if (open[j]) top = max(top, order_key(x[j]));
   }
-  // The softmax's maximum; its sum only where it is used: with renormalised
-  // weights it cancels, and without bias and groups it does not change the
-  // choice.
   float mx = 0.f;
-  T inv_sum = T(1);
+  double inv_sum = 1.0;
   if (!ra.sigmoid) {
-    const uint32_t t = wave_max(top);
-    mx = __builtin_bit_cast(float, (t >> 31) != 0 ? t & 0x7FFFFFFFu : ~t);
-    if (WIDE || !ra.renormalise) {
-      T sum = T(0);
+    mx = key_value(wave_max(top));
+    double sum = 0.0;
 #pragma unroll
-      for (int j = 0; j < NE; ++j)
-        if (open[j]) sum += exp(static_cast<T>(x[j]) - static_cast<T>(mx));
-      sum = wave_sum(sum);
-      inv_sum = sum > T(0) ? T(1) / sum : T(0);
-    }
+    for (int j = 0; j < NE; ++j)
+      if (open[j]) sum += exp(static_cast<double>(x[j]) - static_cast<double>(mx));
+    sum = wave_sum(sum);
+    inv_sum = sum > 0.0 ? 1.0 / sum : 0.0;
   }
-
-  Key key[NE];
-  if constexpr (WIDE) {
-    double c[NE];
+  uint64_t key[NE];
 #pragma unroll
-    for (int j = 0; j < NE; ++j) {
-      const int i = lane * NE + j;
-      c[j] = open[j] ? score_of<double>(x[j], ra.sigmoid, mx, inv_sum) : 0.0;
-      if (open[j] && bias != nullptr) c[j] += static_cast<double>(bias[i]);
-      open[j] = open[j] && c[j] >= -1.7976931348623157e308;  // a bias of -inf or NaN closes its expert
-    }
-    if (ra.groups > 1) {
-      // Group values: 64 / 2^ceil(log2 groups) lanes per group take every
-      // such expert's choice value from LDS and merge their two largest.
-      const double low = -__builtin_inf();
-      double* cv = choice_values + wid * E;
-#pragma unroll
-      for (int j = 0; j < NE; ++j)
-        if (lane * NE + j < E) cv[lane * NE + j] = open[j] ? c[j] : low;
-      wave_sync();
-      const int g = lane >> ra.log2_lanes, lanes_g = 1 << ra.log2_lanes, sub = lane & (lanes_g - 1);
-      double a = low, b = low;  // a >= b
-      if (g < ra.groups) {
-        for (int i = sub; i < ra.per_group; i += lanes_g) {
-          const double v = cv[g * ra.per_group + i];
-          b = fmax(b, fmin(a, v));
-          a = fmax(a, v);
-        }
-      }
-      for (int s = 1; s < lanes_g; s <<= 1) {
-        const double a2 = __shfl_xor(a, s), b2 = __shfl_xor(b, s);
-        b = fmax(fmax(b, b2), fmin(a, a2));
-        a = fmax(a, a2);
-      }
-      uint64_t gk = 0;
-      if (g < ra.groups && sub == 0 && a > low) gk = order_key(b > low ? a + b : a);
-      uint64_t kept = 0;  // (uniform) bit g: group g is kept
-      for (int t = 0; t < ra.top_groups; ++t) {
-        const uint64_t best = wave_max(gk);
-        if (best == 0) break;
-        const int owner = __ffsll(static_cast<unsigned long long>(__ballot(gk == best))) - 1;
-        kept |= uint64_t{1} << (owner >> ra.log2_lanes);
-        if (lane == owner) gk = 0;
-      }
-#pragma unroll
-      for (int j = 0; j < NE; ++j) open[j] = open[j] && ((kept >> ((lane * NE + j) / ra.per_group)) & 1) != 0;
-    }
-#pragma unroll
-    for (int j = 0; j < NE; ++j) key[j] = open[j] ? order_key(c[j]) : 0;
-  } else {
-#pragma unroll
-    for (int j = 0; j < NE; ++j) key[j] = open[j] ? order_key(x[j]) : 0;
+  for (int j = 0; j < NE; ++j) {
+    const int i = lane * NE + j;
+    double c = open[j] ? score(x[j], mx, inv_sum) : 0.0;
+    if (open[j] && bias != nullptr) c += static_cast<double>(bias[i]);
+    open[j] = open[j] && c >= -1.7976931348623157e308;  // a bias of -inf or NaN closes its expert
+    if (ra.groups > 1 && i < E) choice[i] = open[j] ? c : -__builtin_inf();
+    key[j] = open[j] ? order_key(bias != nullptr ? c : static_cast<double>(x[j])) : 0;
   }
-
-  // The k largest, one at a time; lane t keeps the t-th choice.
+  if (ra.groups > 1) {
+    // 64 / 2^ceil(log2 groups) lanes per group merge its two largest values.
+    wave_sync();
+    const double low = -__builtin_inf();
+    int log2_lanes = 6;
+    while ((64 >> log2_lanes) < ra.groups) --log2_lanes;
+    const int g = lane >> log2_lanes, lanes_g = 1 << log2_lanes, sub = lane & (lanes_g - 1);
+    const int per_group = E / ra.groups;
+    double a = low, b = low;  // a >= b
+    if (g < ra.groups) {
+      for (int i = sub; i < per_group; i += lanes_g) {
+        const double v = choice[g * per_group + i];
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
+      }
+    }
+    for (int s = 1; s < lanes_g; s <<= 1) {
+      const double a2 = __shfl_xor(a, s), b2 = __shfl_xor(b, s);
+      b = fmax(fmax(b, b2), fmin(a, a2));
+      a = fmax(a, a2);
+    }
+    uint64_t gk = 0;
+    if (g < ra.groups && sub == 0 && a > low) gk = order_key(b > low ? a + b : a);
+    uint64_t kept = 0;  // (uniform) bit g: group g is kept
+    for (int t = 0; t < ra.top_groups; ++t) {
+      const uint64_t best = wave_max(gk);
+      if (best == 0) break;
+      const int owner = __ffsll(static_cast<unsigned long long>(__ballot(gk == best))) - 1;
+      kept |= uint64_t{1} << (owner >> log2_lanes);
+      if (lane == owner) gk = 0;
+    }
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if (lane * NE + j >= E || ((kept >> ((lane * NE + j) / per_group)) & 1) == 0) key[j] = 0;
+    wave_sync();  // the next row may overwrite the values
+  }
   int mine = -1;
   for (int t = 0; t < ra.k; ++t) {
-    Key best = 0;
+    uint64_t best = 0;
     int at = 0;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
@@ -216,7 +197,7 @@ __global__ __launch_bounds__(64 * kRouteRows) void route_kernel(const L* __restr
         at = j;
       }
     }
-    const Key top_key = wave_max(best);
+    const uint64_t top_key = wave_max(best);
     if (top_key == 0) break;
     const int owner = __ffsll(static_cast<unsigned long long>(__ballot(best == top_key))) - 1;
     const int chosen = owner * NE + __builtin_amdgcn_readlane(at, owner);
@@ -227,40 +208,337 @@ __global__ __launch_bounds__(64 * kRouteRows) void route_kernel(const L* __restr
         if (j == at) key[j] = 0;
     }
   }
-  // Weights of the chosen experts, their sum over the first k lanes in a fixed order.
-  T s = T(0);
-  if (mine >= 0) s = score_of<T>(load_logit(row + mine), ra.sigmoid, mx, inv_sum);
+  double s = mine >= 0 ? score(load_logit(row + mine), mx, inv_sum) : 0.0;
   if (ra.renormalise) {
-    const T total = wave_sum(s);
-    s = total > T(0) ? s / total : T(0);
+    const double total = wave_sum(s);
+    s = total > 0.0 ? s / total : 0.0;
   }
   if (lane < ra.k) {
-    ids[static_cast<int64_t>(m) * ra.k + lane] = mine;
-    weights[static_cast<int64_t>(m) * ra.k + lane] = static_cast<float>(s * static_cast<T>(ra.scale));
+    ids[lane] = mine;
+    weights[lane] = static_cast<float>(s * static_cast<double>(ra.scale));
   }
 }
 
-template <typename L, bool WIDE>
-hipError_t launch_route_typed(const L* logits, int64_t ldl, int64_t M, int64_t E, const float* bias,
-                              const RouteArgs& ra, int32_t* ids, float* weights, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((M + kRouteRows - 1) / kRouteRows)), block(64 * kRouteRows);
-  const size_t lds = ra.groups > 1 ? sizeof(double) * kRouteRows * E : 0;
-  const int m = static_cast<int>(M), e = static_cast<int>(E);
-#define CONVROT_ROUTE(NE_)                                                                                   \
-  hipLaunchKernelGGL((route_kernel<L, NE_, WIDE>), grid, block, lds, stream, logits, ldl, m, e, bias, ra, ids, \
-                     weights)
-  if (E <= 64)
-    CONVROT_ROUTE(1);
-  else if (E <= 128)
-    CONVROT_ROUTE(2);
-  else if (E <= 256)
-    CONVROT_ROUTE(4);
-  else if (E <= 512)
-    CONVROT_ROUTE(8);
-  else
-    CONVROT_ROUTE(16);
-#undef CONVROT_ROUTE
+// Reductions over the L lanes of a row (every lane gets the result).
+template <int L, typename T, typename F>
+__device__ __forceinline__ T row_reduce(T v, F&& f) {
+  auto as = [](uint32_t u) { return __builtin_bit_cast(T, u); };
+  const auto bits = [](T t) { return __builtin_bit_cast(uint32_t, t); };
+  v = f(v, as(lanes::dpp_u<lanes::kQuadXor1>(bits(v))));
+  v = f(v, as(lanes::dpp_u<lanes::kQuadXor2>(bits(v))));
+  v = f(v, as(lanes::dpp_u<lanes::kRowRor4>(bits(v))));
+  v = f(v, as(lanes::dpp_u<lanes::kRowRor8>(bits(v))));
+  if constexpr (L > 16) v = f(v, __shfl_xor(v, 16));
+  if constexpr (L > 32) v = f(v, __shfl_xor(v, 32));
+  return v;
+}
+
+// L: lanes per row (at least k; k + 2 where there is a bias, or every row is
+// done in fp64).
+// NE: experts per lane, in runs of up to four consecutive ones that the lanes
+// of a row take in turn.  WIDE: with a bias or groups; NX: experts per lane of
+// the fp64 path.
+template <typename Lg, int L, int NE, bool WIDE, int NX>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __restrict__ logits, int64_t ldl, int M,
+                                                                 int E, const float* __restrict__ bias, RouteArgs ra,
+                                                                 int32_t* __restrict__ ids,
+                                                                 float* __restrict__ weights) {
+  constexpr int kRows = 64 / L;  // rows per wavefront
+  constexpr int kRun = NE < 4 ? NE : 4;
+  constexpr float kU = 5.9604645e-8f;  // 2^-24
+  constexpr uint64_t kRowLanes = L == 64 ? ~uint64_t{0} : (uint64_t{1} << (L % 64)) - 1;
+  extern __shared__ __attribute__((aligned(16))) double choice_lds[];  // per wavefront, RouteArgs::lds_doubles
+  const int lane = threadIdx.x & 63;
+  const int wid = threadIdx.x >> 6;
+  const int l = lane % L, base = lane - l;  // lane within the row, the row's first lane
+  const int m0 = (blockIdx.x * kRouteWaves + wid) * kRows;
+  if (m0 >= M) return;  // (nothing below synchronises the workgroup)
+  const int m = min(m0 + lane / L, M - 1);  // (rows past the last repeat it and store nothing)
+  const Lg* row = logits + static_cast<int64_t>(m) * ldl;
+  auto expert = [&](int j) { return (j / kRun * L + l) * kRun + j % kRun; };
+  auto max_u = [](uint32_t a, uint32_t b) { return max(a, b); };
+  auto min_i = [](int a, int b) { return min(a, b); };
+  auto add_f = [](float a, float b) { return a + b; };
+  auto max_f = [](float a, float b) { return fmaxf(a, b); };
+
+  float x[NE];
+  typedef Lg run_t __attribute__((ext_vector_type(kRun)));
+#pragma unroll
+  for (int j = 0; j < NE; j += kRun) {
+    const int i = expert(j);
+    if (ra.vec) {
+      run_t v{};
+      if (i < E) v = *reinterpret_cast<const run_t*>(row + i);
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) x[j + e] = i < E ? clamp_logit(static_cast<float>(v[e])) : -__builtin_inff();
+    } else {
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) x[j + e] = i + e < E ? load_logit(row + i + e) : -__builtin_inff();
+    }
+  }
+  uint32_t key[NE];
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    key[j] = open_logit(x[j]) ? order_key(x[j]) : 0;
+    top = max(top, key[j]);
+  }
+  // The softmax's maximum; its sum only where it is used: with renormalised
+  // weights it cancels, and without bias and groups it does not change the
+  // choice.
+  float mx = 0.f, inv_sum = 1.f;
+  if (!ra.sigmoid) {
+    top = row_reduce<L>(top, max_u);
+    mx = top != 0 ? key_value(top) : 0.f;
+    if (WIDE || !ra.renormalise) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NE; ++j)
+        if (key[j] != 0) sum += expf(x[j] - mx);
+      sum = row_reduce<L>(sum, add_f);
+      inv_sum = sum > 0.f ? 1.f / sum : 0.f;
+    }
+  }
+  // Score in fp32, and its error in units of 2^-24.  Logistic: expf is good to
+  // 2 units, the sum and the quotient round once: 5 units of s.  Softmax: the
+  // argument's rounding moves e^-t by t units of itself, i.e. the score by
+  // less than one unit of 1 (t e^-t < 0.4) and the sum by less than ln E units
+  // of itself; at most 22 additions, expf and two roundings: 36 units of s.
+  auto score = [&](float v) {
+    return ra.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - mx) * inv_sum;
+  };
+  const float units = ra.sigmoid ? 5.f : 36.f;
+  auto error = [&](float s, float c) { return kU * (units * s + 1.f + fabsf(c)); };
+
+  bool doubt = false;  // a choice the fp32 values do not settle
+  if constexpr (WIDE) {
+    // (without branches, so that the experts' chains overlap; what belongs to
+    // no open expert is dropped by its key)
+    float c[NE];
+#pragma unroll
+    for (int j = 0; j < NE; ++j) c[j] = score(x[j]);
+    if (bias != nullptr) {
+      typedef float bias_t __attribute__((ext_vector_type(kRun)));
+#pragma unroll
+      for (int j = 0; j < NE; j += kRun) {
+        const int i = expert(j);
+        if (ra.vec_bias) {
+          const bias_t v = *reinterpret_cast<const bias_t*>(bias + min(i, E - kRun));
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) c[j + e] += v[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) c[j + e] += bias[min(i + e, E - 1)];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const bool open = key[j] != 0 && c[j] >= -3.402823466e38f;  // a bias of -inf or NaN closes its expert
+      key[j] = !open ? 0 : bias != nullptr ? order_key(c[j]) : key[j];
+    }
+    if (ra.groups > 1) {
+      // Group values: the row's choice values in LDS, lanes_g lanes per group
+      // (rounds of L / lanes_g groups), then every group's rank by counting.
+      const float low = -__builtin_inff();
+      float* cv = reinterpret_cast<float*>(choice_lds + wid * ra.lds_doubles) + lane / L * (L * NE + 64);
+      float* gv = cv + L * NE;
+#pragma unroll
+      for (int j = 0; j < NE; ++j) cv[expert(j)] = key[j] != 0 ? c[j] : low;
+      wave_sync();
+      const int per_group = E / ra.groups;
+      int lanes_g = L;
+      while (lanes_g > 1 && L / lanes_g < ra.groups) lanes_g >>= 1;
+      float err = 0.f;  // of a group's value: two choice values and their sum
+      const float s_max = ra.sigmoid ? 1.f : inv_sum;
+      for (int g0 = 0; g0 < ra.groups; g0 += L / lanes_g) {
+        const int g = g0 + l / lanes_g;
+        float a = low, b = low;  // a >= b
+        if (g < ra.groups) {
+#pragma unroll 4
+          for (int i = l % lanes_g; i < per_group; i += lanes_g) {
+            const float v = cv[g * per_group + i];
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
+          }
+        }
+        for (int s = 1; s < lanes_g; s <<= 1) {
+          const float a2 = __shfl_xor(a, s), b2 = __shfl_xor(b, s);
+          b = fmaxf(fmaxf(b, b2), fminf(a, a2));
+          a = fmaxf(a, a2);
+        }
+        if (g < ra.groups && l % lanes_g == 0) {
+          gv[g] = b > low ? a + b : a;
+          if (a > low)
+            err = fmaxf(err, 2.f * error(s_max, a) + kU * (b > low ? fabsf(b) + fabsf(a + b) : 0.f));
+        }
+      }
+      wave_sync();
+      uint64_t kept = 0;
+      float worst = -low, best_out = low;  // least kept value, largest one left out
+      for (int g0 = 0; g0 < ra.groups; g0 += L) {
+        const int g = g0 + l;
+        const float v = g < ra.groups ? gv[g] : low;
+        int rank = 0;
+#pragma unroll 8
+        for (int o = 0; o < ra.groups; ++o) {
+          const float w = gv[o];
+          rank += w > v || (w == v && o < g) ? 1 : 0;
+        }
+        const bool keep = v > low && rank < ra.top_groups;
+        if (keep) worst = fminf(worst, v);
+        else best_out = fmaxf(best_out, v);
+        const uint64_t bits = __ballot(keep) >> base;
+        kept |= (bits & kRowLanes) << g0;
+      }
+      worst = -row_reduce<L>(-worst, max_f);
+      best_out = row_reduce<L>(best_out, max_f);
+      err = row_reduce<L>(err, max_f);
+      doubt = best_out > low && worst - best_out <= 2.f * err;
+      // the expert's group, i / per_group, by a product (half a group's width
+      // away from the next integer, exact for these sizes)
+      const float inv_group = 1.f / static_cast<float>(per_group);
+#pragma unroll
+      for (int j = 0; j < NE; ++j) {
+        const int g = static_cast<int>((static_cast<float>(expert(j)) + 0.5f) * inv_group);
+        if (((kept >> (g & 63)) & 1) == 0) key[j] = 0;
+      }
+    }
+  }
+
+  // The k largest, one at a time; lane t of the row keeps the t-th.  Where c
+  // decides, two more are taken: neighbours must differ by more than their
+  // errors, or the first k + 1 are ordered again by their fp64 values.
+  const bool check = WIDE && bias != nullptr;
+  const int picks = ra.k + (check ? 2 : 0);
+  int mine = -1;
+  uint32_t mine_key = 0;
+  for (int t = 0; t < picks; ++t) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) best = max(best, key[j]);
+    best = row_reduce<L>(best, max_u);
+    int at = NE;
+#pragma unroll
+    for (int j = NE - 1; j >= 0; --j)
+      if (key[j] == best) at = j;
+    const int i = at < NE && best != 0 ? (at / kRun * L + l) * kRun + at % kRun : 0x7FFFFFFF;
+    const int chosen = row_reduce<L>(i, min_i);
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if (j == at && i == chosen) key[j] = 0;
+    if (l == t && best != 0) {
+      mine = chosen;
+      mine_key = best;
+    }
+  }
+  float mine_x = mine >= 0 ? load_logit(row + mine) : 0.f;
+  if (check) {
+    const float c = mine >= 0 ? key_value(mine_key) : 0.f;
+    const float err = mine >= 0 ? error(score(mine_x), c) : 0.f;
+    const float c_next = __shfl(c, lane + 1), err_next = __shfl(err, lane + 1);
+    const int next = __shfl(mine, lane + 1);
+    // lane t: its choice and the next are not told apart
+    const bool near = l <= ra.k && mine >= 0 && next >= 0 && c - c_next <= err + err_next;
+    const uint64_t pairs = (__ballot(near) >> base) & kRowLanes;  // of this row
+    const bool reorder = (pairs & ((uint64_t{1} << ra.k) - 1)) != 0;
+    // the set of the first k + 1 is itself in doubt (or has no lane)
+    doubt = doubt || ra.k + 2 > L || ((pairs >> (ra.k - 1)) & 3) == 3;
+    if (__ballot(reorder) != 0) {  // (uniform)
+      double inv = 1.0;
+      if (!ra.sigmoid) {
+        double sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < NE; ++j)
+          if (open_logit(x[j])) sum += exp(static_cast<double>(x[j]) - static_cast<double>(mx));
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) sum += __shfl_xor(sum, d);
+        inv = sum > 0.0 ? 1.0 / sum : 0.0;
+      }
+      double cd = -__builtin_inf();
+      if (mine >= 0 && l <= ra.k) {
+        cd = ra.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(mine_x)))
+                        : exp(static_cast<double>(mine_x) - static_cast<double>(mx)) * inv;
+        cd += static_cast<double>(bias[mine]);
+      }
+      int rank = 0;
+      for (int o = 0; o <= ra.k; ++o) {
+        const double co = __shfl(cd, base + o);
+        const int io = __shfl(mine, base + o);
+        rank += io >= 0 && (co > cd || (co == cd && io < mine)) ? 1 : 0;
+      }
+      int sorted = -1;
+      for (int o = 0; o <= ra.k; ++o) {
+        const int ro = __shfl(rank, base + o), io = __shfl(mine, base + o);
+        if (io >= 0 && ro == l) sorted = io;
+      }
+      if (reorder) {
+        mine = sorted;
+        mine_x = mine >= 0 ? load_logit(row + mine) : 0.f;
+      }
+    }
+  }
+  // Weights of the first k lanes, summed in a fixed order.
+  float s = 0.f;
+  if (mine >= 0 && l < ra.k) s = score(mine_x);
+  if (ra.renormalise) {
+    const float total = row_reduce<L>(s, add_f);
+    s = total > 0.f ? s / total : 0.f;
+  }
+  uint64_t again = 0;  // (uniform) lanes in doubt
+  bool settled = true;
+  if constexpr (WIDE) {
+    again = __ballot(doubt);
+    settled = ((again >> base) & kRowLanes) == 0;
+  }
+  if (l < ra.k && settled && m0 + lane / L < M) {
+    ids[static_cast<int64_t>(m) * ra.k + l] = mine;
+    weights[static_cast<int64_t>(m) * ra.k + l] = s * ra.scale;
+  }
+  if constexpr (WIDE) {
+    if (again != 0) {
+      wave_sync();
+      for (int r = 0; r < kRows && m0 + r < M; ++r) {
+        if (((again >> (r * L)) & kRowLanes) == 0) continue;
+        const int64_t mr = m0 + r;
+        route_row_exact<NX>(logits + mr * ldl, E, bias, ra, choice_lds + wid * ra.lds_doubles, ids + mr * ra.k,
+                            weights + mr * ra.k);
+      }
+    }
+  }
+}
+
+template <typename Lg, bool WIDE, int L, int NE, int NX>
+hipError_t launch_route_typed(const Lg* logits, int64_t ldl, int64_t M, int64_t E, const float* bias, RouteArgs ra,
+                              int32_t* ids, float* weights, hipStream_t stream) {
+  constexpr int64_t rows = kRouteWaves * (64 / L);
+  constexpr int kRun = NE < 4 ? NE : 4;
+  ra.vec = E % kRun == 0 && ldl % kRun == 0 && (reinterpret_cast<uintptr_t>(logits) % (kRun * sizeof(Lg))) == 0;
+  ra.vec_bias = E % kRun == 0 && (reinterpret_cast<uintptr_t>(bias) % (kRun * sizeof(float))) == 0;
+  // fp32 choice and group values of the wavefront's rows, or one row in fp64
+  ra.lds_doubles = ra.groups > 1 ? static_cast<int>(std::max<int64_t>(E, (64 / L * (L * NE + 64) + 1) / 2)) : 0;
+  const size_t lds = sizeof(double) * kRouteWaves * ra.lds_doubles;  // at most 32 KiB
+  hipLaunchKernelGGL((route_kernel<Lg, L, NE, WIDE, NX>), dim3(static_cast<unsigned>((M + rows - 1) / rows)),
+                     dim3(64 * kRouteWaves), lds, stream, logits, ldl, static_cast<int>(M), static_cast<int>(E), bias,
+                     ra, ids, weights);
   return hipGetLastError();
+}
+
+// Sixteen lanes per row up to 14 choices and 256 experts (at most 16 per lane),
+// more lanes above.
+template <typename Lg, bool WIDE>
+hipError_t launch_route_lanes(const Lg* l, int64_t ldl, int64_t M, int64_t E, const float* bias, const RouteArgs& ra,
+                              int32_t* ids, float* weights, hipStream_t s) {
+#define CONVROT_ROUTE(L_, NE_, NX_) return launch_route_typed<Lg, WIDE, L_, NE_, NX_>(l, ldl, M, E, bias, ra, ids, weights, s)
+  if (ra.k <= 14 && E <= 256) {
+    if (E <= 16) CONVROT_ROUTE(16, 1, 1);
+    if (E <= 64) CONVROT_ROUTE(16, 4, 1);
+    if (E <= 128) CONVROT_ROUTE(16, 8, 2);
+    CONVROT_ROUTE(16, 16, 4);
+  }
+  if (ra.k <= 30 && E <= 512) CONVROT_ROUTE(32, 16, 8);
+  CONVROT_ROUTE(64, 16, 16);
+#undef CONVROT_ROUTE
 }
 
 // ---------------------------------------------------------------------------
@@ -501,18 +779,15 @@ hipError_t launch_combine_typed(const T* Y, int64_t ldy, const float* weights, c
 hipError_t launch_route(const void* logits, Elt dt, int64_t ldl, int64_t M, int64_t E, const float* bias,
                         RouteArgs ra, int32_t* ids, float* weights, hipStream_t stream) {
   if (M == 0) return hipSuccess;
-  ra.per_group = static_cast<int>(E) / ra.groups;
-  ra.log2_lanes = 6;
-  while ((64 >> ra.log2_lanes) < ra.groups) --ra.log2_lanes;
   const bool wide = bias != nullptr || ra.groups > 1;
   if (dt == Elt::F32) {
     const auto* l = static_cast<const float*>(logits);
-    return wide ? launch_route_typed<float, true>(l, ldl, M, E, bias, ra, ids, weights, stream)
-                : launch_route_typed<float, false>(l, ldl, M, E, bias, ra, ids, weights, stream);
+    return wide ? launch_route_lanes<float, true>(l, ldl, M, E, bias, ra, ids, weights, stream)
+                : launch_route_lanes<float, false>(l, ldl, M, E, bias, ra, ids, weights, stream);
   }
   const auto* l = static_cast<const __bf16*>(logits);
-  return wide ? launch_route_typed<__bf16, true>(l, ldl, M, E, bias, ra, ids, weights, stream)
-              : launch_route_typed<__bf16, false>(l, ldl, M, E, bias, ra, ids, weights, stream);
+  return wide ? launch_route_lanes<__bf16, true>(l, ldl, M, E, bias, ra, ids, weights, stream)
+              : launch_route_lanes<__bf16, false>(l, ldl, M, E, bias, ra, ids, weights, stream);
 }
 
 // Pairs counted by every workgroup anew, and pairs per chunk.  A chunk's
