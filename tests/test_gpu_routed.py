@@ -345,6 +345,33 @@ def test_lora_add_grouped(cuda, M, E, K, N, r, dt):
     assert torch.equal(yd, out)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [5, 200])
+def test_lora_rows_without_an_adapter_keep_their_bits(cuda, M, dt):
+    """Copied out of place bit for bit, signed zeros, infinities and NaN
+    payloads included; and a bad value in one row, or in an adapter nobody of
+    that row uses, stays in its rows."""
+    E, K, N, r = 3, 64, 40, 16
+    x, a, b, s, y, ids = _adapters(M, E, K, N, r, 8, dt)
+    ids[: M // 2] = np.where(np.arange(M // 2) % 2 == 0, -1, E)
+    ids[M // 2:] = np.arange(M - M // 2) % 2  # adapter 2 is not used
+    y[:, ::7], y[:, 1::7], y[:, 2::7] = -0.0, np.inf, np.nan
+    a[2], b[2] = np.nan, np.inf
+    x[0] = np.nan                # a row without an adapter
+    x[M - 1] = np.inf            # one with
+    t = lambda v, d: torch.from_numpy(np.ascontiguousarray(v)).to(d).to(cuda)
+    yd = t(y, TDT[dt])
+    out = cr.lora_add_grouped(t(x, torch.bfloat16), t(a, torch.bfloat16), t(b, torch.bfloat16), t(s, torch.float32), yd,
+                              cr.group_rows(t(ids, torch.int32), E), out=torch.full_like(yd, 7.0))
+    bits = torch.int16 if dt == "bf16" else torch.int32
+    assert torch.equal(out[: M // 2].view(bits), yd[: M // 2].view(bits))
+    rest = to_np(out[M // 2:M - 1])[:, 3::7]
+    assert np.isfinite(rest).all()
+    keep = slice(M // 2, M - 1)
+    want, bound = R.lora(x[keep], a[:2], b[:2], s[:2], y[keep], ids[keep], dt)
+    _close(rest, want[:, 3::7], bound[:, 3::7])
+
+
 def test_lora_add_grouped_strided(cuda):
     """Operands inside wider buffers and an output off 16 bytes."""
     M, E, K, N, r = 70, 3, 256, 50, 16

@@ -47,6 +47,13 @@ __device__ __forceinline__ void wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 #endif
 }
+// A wavefront's own LDS writes are visible to all its lanes past this point (its
+// LDS operations complete in order; the compiler keeps them so).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 // Workgroup barrier without a fence: callers wait for what they need.
 __device__ __forceinline__ void barrier() {
 #if defined(__HIP_DEVICE_COMPILE__)

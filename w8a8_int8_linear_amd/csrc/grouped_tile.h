@@ -292,6 +292,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a
       m_pos[64 * h + lane_e] = s_pos[h];
       m_row[64 * h + lane_e] = out_row[h];
     }
+    wave_sync();
     f32x4 sc[4], bs[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -353,7 +354,9 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a
         if constexpr (f < kPT) {
           if (f < np) {
             finish(f_c);
+            wave_sync();
             leave(f_c);
+            wave_sync();
           }
         }
       } else {
@@ -363,6 +366,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a
         if constexpr (f > 0) {
           if (f <= np) leave(std::integral_constant<int, f - 1>{});
         }
+        wave_sync();
       }
     });
     if (!more) break;

@@ -319,6 +319,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
         const int piece = 64 * i + lane;
         *reinterpret_cast<f32x4*>(st + piece / kRowPieces * kPitch + piece % kRowPieces * 4) = v[i];
       }
+      wave_sync();
 #pragma unroll
       for (int s = s0; s < s0 + kChunk; ++s) {
         const f32x4* from = reinterpret_cast<const f32x4*>(st + row * kPitch + 32 * (s - s0) + 8 * ch);
@@ -333,11 +334,12 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
           }
         }
       }
+      wave_sync();
     }
   }
 
   const int first = (blockIdx.x % a.col_blocks * (kUpWaves / MT) + wid / MT) * a.col_steps * 64;
-  float* st = stage[wid];  // (a wave's LDS operations complete in order)
+  float* st = stage[wid];
   // A step's pieces of Y and of B; the next step's are requested before this
   // one's are used.  B: fragments, or (kShare) the thread's 16-byte pieces of
   // the 64 rows, lane by lane along a row.
@@ -395,9 +397,10 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
         }
     }
     // Lane holds position w0 + row and features n0 + 16 j + 4 ch + e: staged
-    // as rows in the wave's own area (its LDS operations complete in order).
+    // as rows in the wave's own area.
 #pragma unroll
     for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4*>(st + row * kPitch + 16 * j + 4 * ch) = acc[j];
+    wave_sync();
     const bool full = a.vec && n0 + col + kVec <= a.N;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
@@ -409,6 +412,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
       vec_t v;
 #pragma unroll
       for (int e = 0; e < kVec; ++e) v[e] = static_cast<out_t>(fmaf(scale, d[e], static_cast<float>(f.old[q][e])));
+      if (!adapted) v = f.old[q];  // the same bits
       if (r >= cnt) continue;
       if (full) {
         *reinterpret_cast<vec_t*>(o[q] + n0 + col) = v;
@@ -418,6 +422,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
           if (n0 + col + e < a.N) o[q][n0 + col + e] = v[e];
       }
     }
+    wave_sync();  // the next step overwrites the staged rows
   };
   Step fa, fb;
   load(first, fa);

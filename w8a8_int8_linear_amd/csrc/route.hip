@@ -27,9 +27,8 @@
 #include <atomic>
 #include <type_traits>
 
-#include "device.h"
+#include "grouped_lds.h"
 #include "lanes.h"
-#include "launchers.h"
 
 namespace convrot {
 namespace {
@@ -88,13 +87,6 @@ __device__ __forceinline__ T wave_sum(T v) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
   return v;
-}
-
-// A wavefront's own LDS writes are visible to its lanes past this point.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // +inf counts as the largest finite value (the maximum's exponential is 1); a

@@ -112,7 +112,7 @@ def route(logits: torch.Tensor, top_k: int, score: str = SOFTMAX, bias: torch.Te
 # The plan
 # ---------------------------------------------------------------------------
 
-@dataclass(frozen=True)
+@dataclass(frozen=True, eq=False)
 class RowGroups:
     """The (row, choice) pairs of a batch in the order of their groups
     (convrot_row_groups).  Pair p belongs to row p // per_row; group g's
