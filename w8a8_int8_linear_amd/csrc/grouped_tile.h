@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a
   const int ch16 = ((lane & 7) ^ (lane >> 3)) * 16;
   struct Tile {
     int group, p0, cnt, n_blk;
-    int x_row[kDma];  // the lane's row of the activation in each transfer
+    int x_pos[kDma];  // what names the lane's row of each transfer: position or pair
     int pair[2];      // the pairs of two of the wave's 128 positions
   };
   // Position within the tile of the wave's entry 64 h + lane.
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a
 #pragma unroll
     for (int i = 0; i < kDma; ++i) {
       const int pos = t.p0 + min(8 * (wid + 8 * i) + (lane >> 3), t.cnt - 1);
-      t.x_row[i] = row_of(a.source, pos, a.source == static_cast<int>(RowOrder::Sorted) ? 0 : a.order[pos], a.per_row);
+      t.x_pos[i] = a.source == static_cast<int>(RowOrder::Sorted) ? pos : a.order[pos];
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) t.pair[h] = a.order[t.p0 + min(position(h), t.cnt - 1)];
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a
       const int64_t ld = up ? a.ldb2 : a.ldb;
       w_base[i] = (up ? a.B2 : a.B) + (static_cast<int64_t>(t.group) * a.N + t.n_blk) * ld;
       w_off[i] = static_cast<uint32_t>(min(feat, a.N - t.n_blk - 1)) * static_cast<uint32_t>(ld);
-      x_ptr[i] = a.A + static_cast<int64_t>(t.x_row[i]) * a.lda;
+      x_ptr[i] = a.A + static_cast<int64_t>(row_of(a.source, t.x_pos[i], t.x_pos[i], a.per_row)) * a.lda;
     }
   };
   // Byte of a row that the lane fetches of slice s (in the last slice, chunks
@@ -204,9 +204,9 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a
       s_pos[h] = a.sa[row_of(a.source, pos, cur.pair[h], a.per_row)];
       out_row[h] = row_of(a.dest, pos, cur.pair[h], a.per_row);
     }
-    // The next tile's rows are looked up now and used at this one's end (a
-    // load whose result is waited for inside the slice loop would make every
-    // transfer wait for it).
+    // The next tile's pairs are looked up now and used at this one's end: loads
+    // return in order, so using them here would wait for the last tile's
+    // stores, and waiting inside the slice loop would hold up every transfer.
     const int next = logical + stride;
     const bool more = next < run_end;
     if (more) tile_at(next, cur);
