@@ -1,6 +1,6 @@
 """Plain 64-bit statements of the operators for rows that choose their
-weights, with bounds on the error of a correct fp32 evaluation.  numpy only,
-written from the definitions; nothing here calls the package.
+weights, with bounds on the error of a correct fp32 evaluation.  numpy (and
+torch's fp64 erf), written from the definitions; nothing here calls the package.
 
 Rounding model: u = 2^-24 is half a step of fp32 relative to the value; a
 bf16 result is off by at most 2^-8 of itself on top (half a step)."""
@@ -10,6 +10,7 @@ from __future__ import annotations
 import math
 
 import numpy as np
+import torch
 
 U = 2.0 ** -24
 HALF_STEP = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
@@ -78,8 +79,8 @@ def _activate(z, act):
         return z / (1.0 + np.exp(-z))
     if act == "gelu_tanh":
         return 0.5 * z * (1.0 + np.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z ** 3)))
-    erf = np.vectorize(math.erf, otypes=[np.float64])
-    return 0.5 * z * (1.0 + erf(z / math.sqrt(2.0)))
+    erf = torch.erf(torch.from_numpy(z / math.sqrt(2.0))).numpy()  # fp64, on the CPU
+    return 0.5 * z * (1.0 + erf)
 
 
 def _affine(x, sx, w, sw, b):

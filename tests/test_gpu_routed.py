@@ -185,6 +185,7 @@ def _ids(M, k, E, seed, unused=0.0):
 # tiled kernel), whole and ragged K and N
 PRODUCTS = [(20, 2, 16, 208, 4200, 16, 0.1), (20, 2, 16, 384, 4224, 64, 0), (160, 1, 16, 128, 1350, 64, 0.1),
             (200, 1, 4, 96, 5200, 16, 0.05), (210, 1, 4, 256, 5185, 64, 0.05),
+            (900, 1, 2, 1152, 8200, 64, 0.05), (900, 1, 2, 1168, 8195, 16, 0.0), (460, 2, 3, 1040, 8200, 16, 0.02),
             (1, 1, 1, 16, 1, 16, 0), (1, 8, 128, 256, 96, 256, 0), (2, 2, 8, 1152, 100, 64, 0), (16, 2, 8, 1152, 260, 64, 0.2),
             (5, 3, 4, 48, 33, 16, 0.5), (40, 4, 6, 2048, 130, 256, 0.1), (150, 2, 3, 320, 77, 64, 0.1),
             (300, 1, 2, 1040, 200, 16, 0.0), (513, 2, 4, 1152, 300, 64, 0.05), (7, 2, 300, 256, 40, 64, 0.3),
@@ -239,7 +240,7 @@ def test_linear_gated_grouped(cuda, M, k, E, K, N, G, unused, dt):
         assert np.all(y[~written] == -3.0)
 
 
-@pytest.mark.parametrize("M,E,K,N", [(3, 4, 256, 64), (90, 3, 1152, 130), (700, 2, 512, 272)])
+@pytest.mark.parametrize("M,E,K,N", [(3, 4, 256, 64), (90, 3, 1152, 130), (700, 2, 512, 272), (900, 2, 1152, 8200)])
 def test_groups_carry_the_bits_of_the_linear_of_their_weight(cuda, M, E, K, N):
     """The accumulator is exact and the epilogue the same expression, so a
     group's rows equal the linear of its weight alone, bit for bit."""
@@ -264,11 +265,11 @@ def test_groups_carry_the_bits_of_the_linear_of_their_weight(cuda, M, E, K, N):
         assert torch.equal(yg[rows], cr.linear_gated(sub, we[0], we[1], be, None, "gelu_tanh"))
 
 
-@pytest.mark.parametrize("M,E", [(20, 4), (600, 2)])
-def test_grouped_strided_operands_and_outputs(cuda, M, E):
+@pytest.mark.parametrize("M,E,K,N", [(20, 4, 192, 75), (600, 2, 192, 75), (450, 2, 1152, 8203)])
+def test_grouped_strided_operands_and_outputs(cuda, M, E, K, N):
     """Row pitches above the width, outputs that start off 16 bytes, padding
     left as it was."""
-    K, N, G, k = 192, 75, 64, 2
+    G, k = 64, 2
     ids = _ids(M, k, E, 2, 0.1)
     plan = cr.group_rows(to_dev(ids, torch.int32), E)
     x, sx, w, sw = _codes((M, K), 1), _scales(M, 2, 3.0), _codes((E * N, K), 3), _scales(E * N, 4, 0.08)

@@ -35,14 +35,12 @@ hipError_t launch_ring_typed(GroupedArgs a, const RowPlan& plan, hipStream_t str
   return hipGetLastError();
 }
 
-// The kernel for a launch, by what the host knows of the groups: the number of
-// pairs and groups (rows per group on average).  Measured on one box, 8 to 32
-// groups, K = 1024 to 6912 (us, the ring alone against the other side):
-//   rows per tile of the ring, by rows per group:
+// The ring's form for a launch, by what the host knows of the groups: the
+// number of pairs and groups (rows per group on average).  Measured on one
+// box, 8 to 32 groups, K = 1024 to 6912 (us):
+//   rows per tile, by rows per group:
 //     4 rows   16: 14.0, 32: 14.6, 64: 15.6       8 rows  16: 17.8, 32: 15.9, 64: 16.9
 //     32 rows  16: 24.8, 32: 21.4, 64: 23.2       64 rows 16: 34.8, 32: 28.0, 64: 26.1
-//   tiled kernel against the ring's 64-row tiles:
-//     128 rows 39.7 / 34.6 and 54.7 / 53.7        256 rows 54.3 / 52.7 and 68.5 / 80.0
 //   K shared by the workgroup's waves (2, 4), with fewer workgroups than CUs:
 //     72 workgroups 25.6, 17.9 (2), 16.6 (4)      128: 10.9, 9.3, 9.0
 //     256: 15.1, 13.8, 15.5                       512: 26.6, 26.8, 27.8
@@ -65,9 +63,30 @@ hipError_t launch_ring(const GroupedArgs& a, const RowPlan& plan, hipStream_t st
                     : launch_ring_typed<OUT, GATED, KTAIL, 1, 4, true>(a, plan, stream);
 }
 
+// Whether the tiled kernel is the faster one.  Both costs are estimates in
+// units of 0.1 us, from launches where a 128-byte slice took a CU 1.4 us for a
+// tile of the tiled kernel (with 8 us for its ends, in whole rounds over the
+// CUs) and 0.7 us for a 64-row tile of the ring (with 4 us per launch).  Tiles
+// are counted as if every group had half a tile that is not full.  Tiled
+// against ring where they meet (us; 8 or 32 groups, r rows per group):
+//   gated K = 2048, N = 1024: r 96 52.9 / 45.4, 128 52.8 / 53.8, 192 55.9 / 64.7
+//   K = 1024, N = 2048:       r 128 37.2 / 34.1, 192 38.3 / 42.1
+//   gated K = 1152, N = 6912: r 64 39.0 / 40.1, 96 43.3 / 50.4
+//   K = 6912, N = 1152 (few workgroups): r 128 67.1 / 43.1, 256 71.2 / 50.8
+template <bool GATED>
+bool tiled_is_faster(const GroupedArgs& a, const RowPlan& plan) {
+  const int64_t cus = device_cus(), slices = (a.K + 127) / 128;
+  const int64_t used = std::min<int64_t>(plan.groups, plan.pairs);
+  auto tiles = [&](int64_t rows) { return std::max(used, plan.pairs / rows + used / 2); };
+  auto blocks = [&](int64_t features) { return (a.N + features - 1) / features; };
+  const int64_t tiled = (tiles(256) + used / 16) * blocks(GATED ? 128 : 256);
+  const int64_t ring = tiles(64) * blocks(GATED ? 64 : 128);
+  return (tiled + cus - 1) / cus * (14 * slices + 80) < std::max(ring, cus) * 7 * slices / cus + 40;
+}
+
 template <int OUT, bool GATED>
 hipError_t launch_grouped(const GroupedArgs& a, const RowPlan& plan, hipStream_t stream) {
-  if (plan.pairs / plan.groups >= 192) {
+  if (tiled_is_faster<GATED>(a, plan)) {
     const Elt out = OUT == 0 ? Elt::F32 : Elt::BF16;
     return GATED ? launch_grouped_tile_gated(a, plan, out, stream) : launch_grouped_tile(a, plan, out, stream);
   }
