@@ -225,6 +225,19 @@ __device__ __forceinline__ T row_reduce(T v, F&& f) {
   return v;
 }
 
+// f over v[0 .. N) as a tree (N a power of two), so that the steps overlap.
+template <int N, typename T, typename F>
+__device__ __forceinline__ T tree(const T (&v)[N], F&& f) {
+  if constexpr (N == 1) {
+    return v[0];
+  } else {
+    T h[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) h[i] = f(v[i], v[i + N / 2]);
+    return tree<N / 2>(h, f);
+  }
+}
+
 // L: lanes per row (at least k; k + 2 where there is a bias, or every row is
 // done in fp64).
 // NE: experts per lane, in runs of up to four consecutive ones that the lanes
@@ -292,15 +305,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
     }
   }
   // Score in fp32, and its error in units of 2^-24.  Logistic: expf is good to
-  // 2 units, the sum and the quotient round once: 5 units of s.  Softmax: the
-  // argument's rounding moves e^-t by t units of itself, i.e. the score by
-  // less than one unit of 1 (t e^-t < 0.4) and the sum by less than ln E units
-  // of itself; at most 22 additions, expf and two roundings: 36 units of s.
+  // 2 units of e^-x, the sum and the quotient round once each, so s is off by
+  // s (2 (1 - s) + 2) units, which is at most 2.  Softmax: the argument's
+  // rounding moves e^-t by t units of itself, i.e. the score by less than one
+  // unit of 1 (t e^-t < 0.4) and the sum by less than ln E units of itself; at
+  // most 22 additions, expf and two roundings: 36 units of s.
   auto score = [&](float v) {
     return ra.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - mx) * inv_sum;
   };
-  const float units = ra.sigmoid ? 5.f : 36.f;
-  auto error = [&](float s, float c) { return kU * (units * s + 1.f + fabsf(c)); };
+  auto error = [&](float s, float c) { return kU * ((ra.sigmoid ? 2.1f : 36.f * s + 1.f) + fabsf(c)); };
 
   bool doubt = false;  // a choice the fp32 values do not settle
   if constexpr (WIDE) {
@@ -406,19 +419,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
   int mine = -1;
   uint32_t mine_key = 0;
   for (int t = 0; t < picks; ++t) {
-    uint32_t best = 0;
+    uint32_t best = row_reduce<L>(tree<NE>(key, max_u), max_u);
+    int at[NE];
 #pragma unroll
-    for (int j = 0; j < NE; ++j) best = max(best, key[j]);
-    best = row_reduce<L>(best, max_u);
-    int at = NE;
-#pragma unroll
-    for (int j = NE - 1; j >= 0; --j)
-      if (key[j] == best) at = j;
-    const int i = at < NE && best != 0 ? (at / kRun * L + l) * kRun + at % kRun : 0x7FFFFFFF;
-    const int chosen = row_reduce<L>(i, min_i);
+    for (int j = 0; j < NE; ++j) at[j] = key[j] == best && best != 0 ? expert(j) : 0x7FFFFFFF;
+    const int chosen = row_reduce<L>(tree<NE>(at, min_i), min_i);
 #pragma unroll
     for (int j = 0; j < NE; ++j)
-      if (j == at && i == chosen) key[j] = 0;
+      if (expert(j) == chosen) key[j] = 0;
     if (l == t && best != 0) {
       mine = chosen;
       mine_key = best;
@@ -543,8 +551,7 @@ hipError_t launch_route_lanes(const Lg* l, int64_t ldl, int64_t M, int64_t E, co
 // anew (one launch); for more, a first launch leaves each chunk's counts in
 // the plan and the second adds them up.  No count is added across workgroups
 // by atomics, and pairs keep their order inside a group, so the plan is the
-// same on every run.  Inside a chunk wavefronts take turns: a lane's place is
-// the group's running count plus the lanes below it with the same id.
+// same on every run.
 //   Bound by latency: the starts of the groups and of their tiles in all
 // lists come from one scan (a run of consecutive groups per thread, six sums
 // at once), which costs two barriers instead of three per sum.
@@ -552,6 +559,7 @@ hipError_t launch_route_lanes(const Lg* l, int64_t ldl, int64_t M, int64_t E, co
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanSums = 1 + kPlanLists;  // pairs, and tiles of every list
+constexpr int kPlanWaveBins = 1024;
 
 __device__ __forceinline__ int group_of(int32_t id, int E) { return id < 0 || id >= E ? E : id; }
 
@@ -595,7 +603,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
     for (int i = tid; i < bins * parts; i += kPlanThreads) {
       const int g = i % bins;
       int all = 0, before = 0;
-#pragma unroll 8
+#pragma unroll 16
       for (int c = i / bins; c < chunks; c += parts) {
         const int n = counts[static_cast<int64_t>(c) * bins + g];
         all += n;
@@ -654,7 +662,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
   }
   __syncthreads();
 
-  // This chunk's pairs, 64 per wavefront and turn.
+  // This chunk's pairs, 64 per wavefront at a time: a lane's place is the
+  // group's next place, plus the pairs of the wavefronts before it, plus the
+  // lanes below it with the same group.  With up to kPlanWaveBins groups the
+  // wavefronts leave their counts in LDS and add those before them; with more
+  // they take turns.
+  const bool counted = bins <= kPlanWaveBins;
+  uint16_t* wave_counts = reinterpret_cast<uint16_t*>(sums + kPlanSums * (bins + 1));  // [kPlanWaves][bins]
   for (int base = c0; base < c1; base += kPlanThreads) {
     const int i = base + tid;
     const bool live = i < c1;
@@ -666,15 +680,34 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
       same &= (g & b) != 0 ? set : ~set;
     }
     const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
+    const bool lead = live && rank == 0;  // the first lane of its group
     const int turns = min(kPlanWaves, (c1 - base + 63) / 64);
-    for (int w = 0; w < turns; ++w) {
-      if (w == wid && live) {
-        const int p = place[g];
-        order[p + rank] = i;
-        // the last lane of the group leaves the next place
-        if (__popcll(same) == rank + 1) place[g] = p + rank + 1;
-      }
+    if (counted) {
+      for (int q = tid; q < kPlanWaves * bins; q += kPlanThreads) wave_counts[q] = 0;
       __syncthreads();
+      if (lead) wave_counts[wid * bins + g] = static_cast<uint16_t>(__popcll(same));
+      __syncthreads();
+      if (live) {
+        int p = place[g] + rank;
+#pragma unroll 4
+        for (int w = 0; w < wid; ++w) p += wave_counts[w * bins + g];
+        order[p] = i;
+      }
+      if (base + kPlanThreads < c1) {  // (uniform) the next 1024 pairs' places
+        __syncthreads();
+        if (lead) atomicAdd(&place[g], static_cast<int>(__popcll(same)));
+        __syncthreads();
+      }
+    } else {
+      for (int w = 0; w < turns; ++w) {
+        if (w == wid && live) {
+          const int p = place[g];
+          order[p + rank] = i;
+          // the last lane of the group leaves the next place
+          if (__popcll(same) == rank + 1) place[g] = p + rank + 1;
+        }
+        __syncthreads();
+      }
     }
   }
 
@@ -689,7 +722,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
       tiles[kPlanLists + b] = total;
     }
     int32_t* list = tiles + plan_list_at(pairs, E, b);
-    for (int t = blockIdx.x * kPlanThreads + tid; t < total; t += gridDim.x * kPlanThreads) {
+    // (another workgroup starts each list)
+    const int turn = (blockIdx.x + b * (gridDim.x / kPlanLists + 1)) % gridDim.x;
+    for (int t = turn * kPlanThreads + tid; t < total; t += gridDim.x * kPlanThreads) {
       int lo = 0, hi = bins - 1;  // the last group that starts at or before tile t
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -804,11 +839,15 @@ hipError_t launch_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32
   int32_t* counts = pairs > kPlanRecount ? tiles + plan_list_at(pairs, E, kPlanLists) : nullptr;
   if (counts != nullptr)
     hipLaunchKernelGGL(plan_count_kernel, grid, dim3(kPlanThreads), 4 * (E + 1), stream, ids, p, e, chunk, counts);
-  const size_t lds = 4 * (E + 1 + kPlanSums * (E + 2));
+  auto lds_bytes = [](int64_t groups) {
+    const int64_t bins = groups + 1;
+    return 4 * (bins + kPlanSums * (bins + 1)) + (bins <= kPlanWaveBins ? 2 * kPlanWaves * bins : 0);
+  };
+  const size_t lds = lds_bytes(E);
   if (lds > 65536 - 1024) {  // more than about 2300 groups
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t err = set_lds_limit(reinterpret_cast<const void*>(plan_order_kernel),
-                                         4 * (kPlanMaxGroups + 1 + kPlanSums * (kPlanMaxGroups + 2)), lds_set);
+                                         static_cast<int>(lds_bytes(kPlanMaxGroups)), lds_set);
     if (err != hipSuccess) return err;
   }
   hipLaunchKernelGGL(plan_order_kernel, grid, dim3(kPlanThreads), lds, stream, ids, p, e, chunk, counts, order,
