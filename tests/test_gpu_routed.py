@@ -312,6 +312,22 @@ def test_combine_rows(cuda, M, k, N, dt):
         assert torch.all(buf[:, 0] == -3.0) and torch.all(buf[:, 1 + N:] == -3.0)
 
 
+def test_combine_more_outputs_than_one_grid_of_threads(cuda):
+    """More outputs than a launch has threads (2^32), a width that takes no
+    16-byte pieces."""
+    M, N = 1 << 22, 1027
+    y = torch.full((M, N), 2.0, dtype=torch.bfloat16, device=cuda)
+    y[-1], y[M // 2, 5] = 3.0, -1.0
+    w = torch.full((M, 1), 0.5, device=cuda)
+    ids = torch.zeros((M, 1), dtype=torch.int32, device=cuda)
+    ids[7] = -1
+    out = torch.full_like(y, 9.0)
+    cr.combine_rows(y, w, ids, 1, out=out)
+    y *= 0.5
+    y[7] = 0.0
+    assert torch.equal(out, y)
+
+
 # ------------------------------------------------------------- adapters per row
 
 def _adapters(M, E, K, N, r, seed, dt):
@@ -373,6 +389,25 @@ def test_lora_rows_without_an_adapter_keep_their_bits(cuda, M, dt):
     _close(rest, want[:, 3::7], bound[:, 3::7])
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("M,E", [(3, 2), (150, 2)])
+def test_lora_infinite_products_stay_infinities(cuda, M, E, dt):
+    """An infinite T (its terms would otherwise be inf and inf - inf)."""
+    K, N, r = 96, 70, 32
+    x, a, b, s, y, ids = _adapters(M, E, K, N, r, 21, dt)
+    ids[:] = np.arange(M) % E
+    a[:, :, 5], b = (to_bf16_values(np.abs(v) + np.float32(0.125)) for v in (a[:, :, 5], b))
+    x[::2, 5] = np.inf
+    x[1, 5] = -np.inf
+    out = cr.lora_add_grouped(*(to_dev(t, torch.bfloat16) for t in (x, a, b)), to_dev(s, torch.float32),
+                              to_dev(y, TDT[dt]), cr.group_rows(to_dev(ids, torch.int32), E))
+    got = to_np(out)
+    assert np.all(got[::2] == np.inf) and np.all(got[1] == -np.inf)
+    rest = np.arange(3, M, 2)
+    want, bound = R.lora(x[rest], a, b, s, y[rest], ids[rest], dt)
+    _close(got[rest], want, bound)
+
+
 def test_lora_add_grouped_strided(cuda):
     """Operands inside wider buffers and an output off 16 bytes."""
     M, E, K, N, r = 70, 3, 256, 50, 16
@@ -389,6 +424,12 @@ def test_lora_add_grouped_strided(cuda):
     got = to_np(yb)
     _close(got[:, 3:3 + N], want, bound)
     assert np.all(got[:, :3] == -3.0) and np.all(got[:, 3 + N:] == -3.0)
+    # Y and out as column slices of one buffer
+    both = torch.zeros((M, 2 * N), dtype=torch.bfloat16, device=cuda)
+    both[:, :N] = to_dev(y, torch.bfloat16)
+    cr.lora_add_grouped(xb[:, :K], ab[:, :r, :K], bb[:, :N, :r], to_dev(s, torch.float32), both[:, :N], plan,
+                        out=both[:, N:])
+    assert torch.equal(both[:, N:], yb[:, 3:3 + N]) and torch.equal(both[:, :N], to_dev(y, torch.bfloat16))
 
 
 def test_layer_with_an_adapter_bank(cuda):

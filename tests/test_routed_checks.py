@@ -137,7 +137,9 @@ def test_empty_products_are_no_ops(lib):
     (INVALID, dict(E=4097)), (INVALID, dict(ldy=7)), (INVALID, dict(ldo=7)), (INVALID, dict(Y=None)),
     (INVALID, dict(out=None)), (INVALID, dict(w=None)), (INVALID, dict(ids=None)), (ALIGN, dict(w=MIS4)),
     (ALIGN, dict(ids=MIS4)), (ALIGN, dict(Y=0x10002, dt=0)), (INVALID, dict(M=1 << 22, k=1, N=(1 << 31) - 1, ldy=1 << 31,
-                                                                           ldo=1 << 31))])
+                                                                           ldo=1 << 31)),
+    (INVALID, dict(out=A)), (INVALID, dict(out=A, k=1)), (INVALID, dict(out=A + 2 * 46)), (INVALID, dict(out=A - 2 * 18)),
+    (INVALID, dict(Y=A, out=A - 64, ldo=1 << 62))])
 def test_combine_checks(lib, want, kw):
     a = dict(Y=A, dt=_lib.BF16, ldy=8, w=B, ids=C, M=3, k=2, N=8, E=4, out=D, ldo=8)
     a.update(kw)
@@ -152,7 +154,8 @@ def test_combine_checks(lib, want, kw):
     (ALIGN, dict(X=MIS16)), (ALIGN, dict(A=MIS16)), (ALIGN, dict(B=MIS16)), (INVALID, dict(sa=16 * 256 - 8)),
     (INVALID, dict(sb=40 * 16 - 8)), (ALIGN, dict(sa=16 * 256 + 4)), (INVALID, dict(scales=None)),
     (ALIGN, dict(scales=MIS4)), (INVALID, dict(ws=None)), (INVALID, dict(wn=64)), (ALIGN, dict(ws=0x90008)),
-    (INVALID, dict(out=0x500000 + 80)), (INVALID, dict(out=0x500000, ldo=48)), (INVALID, dict(Y=None))])
+    (INVALID, dict(out=0x500000 + 80)), (INVALID, dict(ldx=(1 << 62) + 256)), (INVALID, dict(lda=(1 << 62) + 256)),
+    (INVALID, dict(out=0x4FFFC0, ldo=1 << 62)), (INVALID, dict(out=0x500000, ldo=48)), (INVALID, dict(Y=None))])
 def test_lora_add_grouped_checks(lib, want, kw):
     a = dict(X=A, ldx=256, M=32, K=256, A=B, lda=256, sa=16 * 256, B=C, ldb=16, sb=40 * 16, N=40, r=16, scales=D,
              p=None, Y=0x500000, ldy=40, dt=_lib.BF16, out=0x600000, ldo=40, ws=0x700000, wn=1 << 30)
@@ -200,6 +203,14 @@ def test_binding_refuses_host_tensors_and_wrong_types():
                  lambda: cr.lora_add_grouped(torch.zeros(4, 16, dtype=torch.bfloat16), None, None, None, None, None)):
         with pytest.raises(ValueError, match="device"):
             call()
+
+
+@pytest.mark.parametrize("kw", [dict(top_k=0), dict(top_k=9), dict(top_k=(1 << 32) + 2), dict(groups=(1 << 32) + 1),
+                                dict(groups=0), dict(top_groups=(1 << 32) + 1)])
+def test_binding_route_sizes(kw):
+    """Sizes a 32-bit field would wrap are refused before it is filled."""
+    with pytest.raises(ValueError, match="experts"):
+        cr.route(torch.zeros(2, 8), **(dict(top_k=2) | kw))
 
 
 @pytest.mark.parametrize("kw,match", [

@@ -949,6 +949,26 @@ convrot_status check_grid(const char* what, int64_t blocks) {
   return CONVROT_OK;
 }
 
+// Whether two matrices of `cols` columns share memory (column slices of one
+// wider matrix do not).
+bool overlap(const void* p, int64_t rows_p, int64_t ldp, const void* q, int64_t rows_q, int64_t ldq, int64_t cols,
+             int64_t elt) {
+  if (rows_p <= 0 || rows_q <= 0 || cols <= 0) return false;
+  if (ldp == ldq) {
+    const __int128 pitch = static_cast<__int128>(ldp) * elt;
+    __int128 apart = (static_cast<__int128>(reinterpret_cast<uintptr_t>(q)) -
+                      static_cast<__int128>(reinterpret_cast<uintptr_t>(p))) % pitch;
+    if (apart < 0) apart += pitch;
+    if (apart >= cols * elt && apart <= pitch - cols * elt) return false;
+  }
+  auto end = [&](const void* a, int64_t rows, int64_t ld) {
+    return static_cast<__int128>(reinterpret_cast<uintptr_t>(a)) +
+           (static_cast<__int128>(rows - 1) * ld + cols) * elt;
+  };
+  return static_cast<__int128>(reinterpret_cast<uintptr_t>(p)) < end(q, rows_q, ldq) &&
+         static_cast<__int128>(reinterpret_cast<uintptr_t>(q)) < end(p, rows_p, ldp);
+}
+
 // Checks of one weight of a grouped linear: as check_linear, with the row
 // counts of a plan in place of M and N.
 convrot_status check_grouped(const char* what, const convrot_packed* act, const convrot_packed* w, const float* bias,
@@ -1112,6 +1132,8 @@ convrot_status convrot_combine_rows(const void* Y, convrot_dtype dt, int64_t ldy
     return fail(CONVROT_ERR_INVALID_ARG, "%s: weights or ids is NULL", what);
   if ((reinterpret_cast<uintptr_t>(weights) & 3u) != 0 || (reinterpret_cast<uintptr_t>(ids) & 3u) != 0)
     return fail(CONVROT_ERR_ALIGN, "%s: weights and ids must be 4-byte aligned", what);
+  if (overlap(Y, M * k, ldy, out, M, ldo, N, elt_size(dt)))
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: out overlaps Y", what);
   st = check_grid(what, M * ((N + 255) / 256));
   if (st != CONVROT_OK) return st;
   return from_hip(convrot::launch_combine_rows(Y, static_cast<convrot::Elt>(dt), ldy, weights, ids, M, k, N, groups,
@@ -1158,12 +1180,12 @@ convrot_status convrot_lora_add_grouped(const void* X, int64_t ldx, int64_t M, i
   if (st != CONVROT_OK) return st;
   st = check_matrix("out", out, M, N, ldo, elt_size(dt), false);
   if (st != CONVROT_OK) return st;
-  if (2 * ldx > kMaxLdBytes || 2 * lda > kMaxLdBytes)
+  if (ldx > kMaxLdBytes / 2 || lda > kMaxLdBytes / 2)
     return fail(CONVROT_ERR_INVALID_ARG, "leading dimension of X or A exceeds %lld bytes",
                 static_cast<long long>(kMaxLdBytes));
   if (stride_a < r * lda || stride_b / ldb < N)
     return fail(CONVROT_ERR_INVALID_ARG, "%s: adapters overlap (stride_a < r * lda or stride_b < N * ldb)", what);
-  if ((2 * stride_a) % 16 != 0 || (2 * stride_b) % 16 != 0)
+  if (stride_a % 8 != 0 || stride_b % 8 != 0)
     return fail(CONVROT_ERR_ALIGN, "%s: the adapters must lie a multiple of 16 bytes apart", what);
   if (M == 0 || N == 0) return ok();
   if (scales == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: scales is NULL", what);
@@ -1171,12 +1193,8 @@ convrot_status convrot_lora_add_grouped(const void* X, int64_t ldx, int64_t M, i
     return fail(CONVROT_ERR_ALIGN, "%s: scales must be 4-byte aligned", what);
   if (out == Y) {
     if (ldo != ldy) return fail(CONVROT_ERR_INVALID_ARG, "%s: out is Y but ldo != ldy", what);
-  } else {
-    const auto* y = static_cast<const char*>(Y);
-    const auto* o = static_cast<const char*>(out);
-    const int64_t elt = elt_size(dt);
-    if (y < o + ((M - 1) * ldo + N) * elt && o < y + ((M - 1) * ldy + N) * elt)
-      return fail(CONVROT_ERR_INVALID_ARG, "%s: out overlaps Y without being Y", what);
+  } else if (overlap(Y, M, ldy, out, M, ldo, N, elt_size(dt))) {
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: out overlaps Y without being Y", what);
   }
   st = check_workspace(workspace, workspace_bytes, convrot::lora_grouped_ws_bytes(M, K, r, groups->groups));
   if (st != CONVROT_OK) return st;

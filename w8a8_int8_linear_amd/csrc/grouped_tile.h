@@ -22,6 +22,14 @@
 // in contiguous runs of (tile, weight block), the weight blocks innermost, so
 // that the blocks that read a tile's rows and the tiles that read a group's
 // weights meet in one L2.
+//
+// Bound by the matrix products inside a tile (a 128-byte slice of a tile with
+// 205 positions in use takes 1.4 us, 1.0 us at the rate of a large library
+// product) and by its ends, about 9.5 us per tile: the epilogue's arithmetic,
+// its stores, and the first slices of the next tile.  128 groups with 65536
+// pairs unevenly over them, bf16: gated K = 2048, N = 768 (412 GOP) 236-244
+// us, 1.7 POPS; K = 768, N = 2048 (206 GOP) 190 us, 1.1 POPS.  Non-temporal
+// stores were 1-2 % faster alone, but take from L2 what the next launch reads.
 #pragma once
 #include "grouped_lds.h"
 
@@ -51,8 +59,8 @@ __device__ __forceinline__ void wait_stores(int np) {
 }
 
 // OUT: 0 = fp32, 1 = bf16.  ACT: activation (the epilogue is unrolled over 128
-// outputs per lane; a run-time choice per output made it several times as long
-// and the kernel 13 us per tile slower).  KTAIL: K is no multiple of 128.
+// outputs per lane, and a run-time choice per output made it 13 us per tile
+// longer).  KTAIL: K is no multiple of 128.
 template <int OUT, int ACT, bool GATED, bool KTAIL>
 __global__ __launch_bounds__(kThreads, 1) void grouped_tile_kernel(GroupedArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];

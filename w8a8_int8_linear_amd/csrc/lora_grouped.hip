@@ -330,7 +330,8 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
 #pragma unroll
           for (int q = 0; q < kTerms; ++q) {
             t[s][q][e] = static_cast<__bf16>(rest);
-            rest -= static_cast<float>(t[s][q][e]);
+            const float term = static_cast<float>(t[s][q][e]);
+            rest = fabsf(term) <= 3.402823466e38f ? rest - term : 0.f;  // nothing follows an infinity or a NaN
           }
         }
       }

@@ -82,6 +82,10 @@ def route(logits: torch.Tensor, top_k: int, score: str = SOFTMAX, bias: torch.Te
     (convrot_route has the rule).  Ties go to the lowest index; a logit of
     -inf closes an expert, and where too few are left the id is -1 and the
     weight 0."""
+    experts = logits.shape[-1] if logits.dim() else 0
+    for n, name in ((top_k, "top_k"), (groups, "groups"), (top_groups, "top_groups")):
+        if not 1 <= n <= experts:
+            raise ValueError(f"{name} must be 1 to the {experts} experts")
     _need_cuda(logits, "logits")
     _need_float(logits, "logits")
     if score not in _SCORE:
@@ -91,8 +95,6 @@ def route(logits: torch.Tensor, top_k: int, score: str = SOFTMAX, bias: torch.Te
     if bias is not None:
         _dense(bias, torch.float32, (E,), "bias")
         _need_device(bias, dev, "bias")
-    if top_k < 1:
-        raise ValueError("top_k must be positive")
     if ids is None:
         ids = torch.empty((M, top_k), dtype=torch.int32, device=dev)
     if weights is None:
