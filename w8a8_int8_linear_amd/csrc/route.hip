@@ -556,10 +556,10 @@ hipError_t launch_route_lanes(const Lg* l, int64_t ldl, int64_t M, int64_t E, co
 // lists come from one scan (a run of consecutive groups per thread, six sums
 // at once), which costs two barriers instead of three per sum.  65536 pairs of
 // 256 groups: 2.7 us to count, 11.1 us to order (13 us with the wavefronts of
-// a chunk in turn); one token's: 8.8 us.
+// a chunk in turn); one token's eight pairs: 5.4 us (9.2 us with 1024 threads
+// and the tile lists one after the other).
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanSums = 1 + kPlanLists;  // pairs, and tiles of every list
 constexpr int kPlanWaveBins = 1024;
 
@@ -576,23 +576,29 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(const int32_t*
   for (int i = threadIdx.x; i <= E; i += kPlanThreads) counts[static_cast<int64_t>(blockIdx.x) * (E + 1) + i] = hist[i];
 }
 
-// counts: the chunks' counts of plan_count_kernel, or NULL to count the ids.
-__global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t* __restrict__ ids, int pairs, int E,
+// T: threads.  counts: the chunks' counts of plan_count_kernel, or NULL to
+// count the ids.
+template <int T>
+__global__ __launch_bounds__(T) void plan_order_kernel(const int32_t* __restrict__ ids, int pairs, int E,
                                                                   int chunk, const int32_t* __restrict__ counts,
                                                                   int32_t* __restrict__ order,
                                                                   int32_t* __restrict__ offsets,
                                                                   int32_t* __restrict__ tiles) {
+  constexpr int kWaves = T / 64;
   extern __shared__ int32_t lds[];
   const int bins = E + 1;
   int32_t* place = lds;          // [bins]: pairs before this chunk, then this chunk's next place
   int32_t* sums = place + bins;  // [kPlanSums][bins + 1]: sums[0] first the pairs per group
-  __shared__ int32_t part[kPlanSums][kPlanWaves];
+  __shared__ int32_t part[kPlanSums][kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
   const int c0 = blockIdx.x * chunk, c1 = min(pairs, c0 + chunk);
-  for (int i = tid; i < bins; i += kPlanThreads) sums[i] = place[i] = 0;
+  for (int i = tid; i < bins; i += T) sums[i] = place[i] = 0;
   __syncthreads();
+  // (requested with the counts; used when the places are known)
+  const int first_group = c0 + tid < c1 ? group_of(ids[c0 + tid], E) : bins;
   if (counts == nullptr) {
-    for (int i = tid; i < pairs; i += kPlanThreads) {
+#pragma unroll 4
+    for (int i = tid; i < pairs; i += T) {
       const int g = group_of(ids[i], E);
       atomicAdd(&sums[g], 1);
       if (i < c0) atomicAdd(&place[g], 1);
@@ -601,8 +607,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
     // Every group's counts of all chunks and of those before this one; with
     // few groups the threads share out the chunks too.
     const int chunks = gridDim.x, me = blockIdx.x;
-    const int parts = max(1, kPlanThreads / bins);
-    for (int i = tid; i < bins * parts; i += kPlanThreads) {
+    const int parts = max(1, T / bins);
+    for (int i = tid; i < bins * parts; i += T) {
       const int g = i % bins;
       int all = 0, before = 0;
 #pragma unroll 16
@@ -617,7 +623,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
   }
   __syncthreads();
   // Exclusive scans over the groups: thread t owns groups t per .. + per - 1.
-  const int per = (bins + kPlanThreads - 1) / kPlanThreads;
+  const int per = (bins + T - 1) / T;
   int own[kPlanSums] = {};
   for (int i = tid * per; i < min(bins, (tid + 1) * per); ++i) {
     const int n = sums[i];
@@ -642,7 +648,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
   for (int q = 0; q < kPlanSums; ++q) {
     int before = 0;
 #pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) before += w < wid ? part[q][w] : 0;
+    for (int w = 0; w < kWaves; ++w) before += w < wid ? part[q][w] : 0;
     upto[q] += before - own[q];
   }
   for (int i = tid * per; i < min(bins, (tid + 1) * per); ++i) {
@@ -670,11 +676,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
   // wavefronts leave their counts in LDS and add those before them; with more
   // they take turns.
   const bool counted = bins <= kPlanWaveBins;
-  uint16_t* wave_counts = reinterpret_cast<uint16_t*>(sums + kPlanSums * (bins + 1));  // [kPlanWaves][bins]
-  for (int base = c0; base < c1; base += kPlanThreads) {
+  uint16_t* wave_counts = reinterpret_cast<uint16_t*>(sums + kPlanSums * (bins + 1));  // [kWaves][bins]
+  for (int base = c0; base < c1; base += T) {
     const int i = base + tid;
     const bool live = i < c1;
-    const int g = live ? group_of(ids[i], E) : bins;
+    const int g = base == c0 ? first_group : live ? group_of(ids[i], E) : bins;
     // lanes with the same group
     uint64_t same = __ballot(live);
     for (int b = 1; b <= E; b <<= 1) {
@@ -683,9 +689,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
     }
     const int rank = __popcll(same & ((uint64_t{1} << lane) - 1));
     const bool lead = live && rank == 0;  // the first lane of its group
-    const int turns = min(kPlanWaves, (c1 - base + 63) / 64);
+    const int turns = min(kWaves, (c1 - base + 63) / 64);
     if (counted) {
-      for (int q = tid; q < kPlanWaves * bins; q += kPlanThreads) wave_counts[q] = 0;
+      for (int q = tid; q < kWaves * bins; q += T) wave_counts[q] = 0;
       __syncthreads();
       if (lead) wave_counts[wid * bins + g] = static_cast<uint16_t>(__popcll(same));
       __syncthreads();
@@ -695,7 +701,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
         for (int w = 0; w < wid; ++w) p += wave_counts[w * bins + g];
         order[p] = i;
       }
-      if (base + kPlanThreads < c1) {  // (uniform) the next 1024 pairs' places
+      if (base + T < c1) {  // (uniform) the next 1024 pairs' places
         __syncthreads();
         if (lead) atomicAdd(&place[g], static_cast<int>(__popcll(same)));
         __syncthreads();
@@ -715,26 +721,30 @@ __global__ __launch_bounds__(kPlanThreads) void plan_order_kernel(const int32_t*
 
   // Tile lists: for rows-per-tile 16 << b, every group cut evenly into as few
   // tiles as hold it, the ungrouped positions (group E) last; entry {group,
-  // first position}.  The lists are shared out over the workgroups.
-  for (int b = 0; b < kPlanLists; ++b) {
-    const int32_t* first = sums + (1 + b) * (bins + 1);
-    const int total = first[bins];
-    if (blockIdx.x == 0 && tid == 0) {
-      tiles[b] = first[E];
-      tiles[kPlanLists + b] = total;
+  // first position}.  Sixteen lanes take sixteen entries; they are shared out
+  // over the lists, which are written side by side.
+  constexpr int kUnits = T / 16 / kPlanLists;  // per list and workgroup
+  const int unit = tid / 16;
+  if (blockIdx.x == 0 && tid < kPlanLists) {
+    tiles[tid] = sums[(1 + tid) * (bins + 1) + E];
+    tiles[kPlanLists + tid] = sums[(1 + tid) * (bins + 1) + bins];
+  }
+  if (unit >= kUnits * kPlanLists) return;
+  const int b = unit % kPlanLists;
+  const int32_t* first = sums + (1 + b) * (bins + 1);
+  int64_t at = 0;  // (by constants: a division by 16 << b would take longer than the search)
+#pragma unroll
+  for (int q = 0; q < kPlanLists; ++q) at = b == q ? plan_list_at(pairs, E, q) : at;
+  int32_t* list = tiles + at;
+  const int total = first[bins], stride = gridDim.x * kUnits * 16;
+  for (int t = (static_cast<int>(blockIdx.x) * kUnits + unit / kPlanLists) * 16 + tid % 16; t < total; t += stride) {
+    int lo = 0, hi = bins - 1;  // the last group that starts at or before tile t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= t) lo = mid; else hi = mid - 1;
     }
-    int32_t* list = tiles + plan_list_at(pairs, E, b);
-    // (another workgroup starts each list)
-    const int turn = (blockIdx.x + b * (gridDim.x / kPlanLists + 1)) % gridDim.x;
-    for (int t = turn * kPlanThreads + tid; t < total; t += gridDim.x * kPlanThreads) {
-      int lo = 0, hi = bins - 1;  // the last group that starts at or before tile t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      list[2 * t] = lo;
-      list[2 * t + 1] = sums[lo] + (t - first[lo]) * plan_tile_rows(sums[lo + 1] - sums[lo], b);
-    }
+    list[2 * t] = lo;
+    list[2 * t + 1] = sums[lo] + (t - first[lo]) * plan_tile_rows(sums[lo + 1] - sums[lo], b);
   }
 }
 
@@ -826,6 +836,11 @@ hipError_t launch_route(const void* logits, Elt dt, int64_t ldl, int64_t M, int6
 // turns are serial, and every workgroup reads all chunks' counts: 1024 pairs
 // (16 turns) where the counts are added, 256 where each workgroup counts.
 static constexpr int64_t kPlanRecount = 8192;
+// 256 threads where the pairs and the groups are few (barriers and the scan over
+// wavefronts are what costs), 1024 otherwise (us, 256 and 1024 threads): 8 pairs
+// of 128 groups 5.4, 6.8; 512 of 256 7.3, 7.7; 2048 of 128 6.7, 7.7; 4096 of 128
+// 7.8, 8.0; 2048 of 1023 9.4, 9.2; 8192 of 256 10.3, 9.1.
+static constexpr int64_t kPlanSmall = 4096, kPlanSmallGroups = 512;
 static int64_t plan_chunk(int64_t pairs) {
   const int64_t c = (pairs + kPlanMaxChunks - 1) / kPlanMaxChunks;
   return std::max<int64_t>(pairs > kPlanRecount ? 1024 : 256, (c + 63) / 64 * 64);
@@ -836,6 +851,25 @@ int64_t plan_ints(int64_t pairs, int64_t E) {
          (pairs > kPlanRecount ? (pairs + plan_chunk(pairs) - 1) / plan_chunk(pairs) * (E + 1) : 0);
 }
 
+template <int T>
+static hipError_t launch_plan_order(dim3 grid, const int32_t* ids, int pairs, int E, int chunk, const int32_t* counts,
+                                    int32_t* order, int32_t* offsets, int32_t* tiles, hipStream_t stream) {
+  auto lds_bytes = [](int groups) {
+    const int bins = groups + 1;
+    return 4 * (bins + kPlanSums * (bins + 1)) + (bins <= kPlanWaveBins ? 2 * (T / 64) * bins : 0);
+  };
+  const int lds = lds_bytes(E);
+  if (lds > 65536 - 1024) {  // more than about 2300 groups
+    static std::atomic<uint64_t> lds_set{0};
+    const hipError_t err = set_lds_limit(reinterpret_cast<const void*>(plan_order_kernel<T>),
+                                         lds_bytes(static_cast<int>(kPlanMaxGroups)), lds_set);
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL(plan_order_kernel<T>, grid, dim3(T), lds, stream, ids, pairs, E, chunk, counts, order, offsets,
+                     tiles);
+  return hipGetLastError();
+}
+
 hipError_t launch_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32_t* order, int32_t* offsets,
                              int32_t* tiles, hipStream_t stream) {
   const int chunk = static_cast<int>(plan_chunk(pairs));
@@ -844,20 +878,9 @@ hipError_t launch_group_rows(const int32_t* ids, int64_t pairs, int64_t E, int32
   int32_t* counts = pairs > kPlanRecount ? tiles + plan_list_at(pairs, E, kPlanLists) : nullptr;
   if (counts != nullptr)
     hipLaunchKernelGGL(plan_count_kernel, grid, dim3(kPlanThreads), 4 * (E + 1), stream, ids, p, e, chunk, counts);
-  auto lds_bytes = [](int64_t groups) {
-    const int64_t bins = groups + 1;
-    return 4 * (bins + kPlanSums * (bins + 1)) + (bins <= kPlanWaveBins ? 2 * kPlanWaves * bins : 0);
-  };
-  const size_t lds = lds_bytes(E);
-  if (lds > 65536 - 1024) {  // more than about 2300 groups
-    static std::atomic<uint64_t> lds_set{0};
-    const hipError_t err = set_lds_limit(reinterpret_cast<const void*>(plan_order_kernel),
-                                         static_cast<int>(lds_bytes(kPlanMaxGroups)), lds_set);
-    if (err != hipSuccess) return err;
-  }
-  hipLaunchKernelGGL(plan_order_kernel, grid, dim3(kPlanThreads), lds, stream, ids, p, e, chunk, counts, order,
-                     offsets, tiles);
-  return hipGetLastError();
+  if (pairs <= kPlanSmall && E <= kPlanSmallGroups)
+    return launch_plan_order<256>(grid, ids, p, e, chunk, counts, order, offsets, tiles, stream);
+  return launch_plan_order<kPlanThreads>(grid, ids, p, e, chunk, counts, order, offsets, tiles, stream);
 }
 
 hipError_t launch_combine_rows(const void* Y, Elt dt, int64_t ldy, const float* weights, const int32_t* ids,
