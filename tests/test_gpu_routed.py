@@ -487,6 +487,18 @@ def test_experts_layer(cuda, M):
     assert torch.equal(layer(x.reshape(1, M, K)).reshape(M, N), out)
 
 
+def test_layers_take_no_rows(cuda):
+    E, K = 4, 256
+    layer = _experts(cuda, E, K, 192, 136, 2)
+    assert layer(torch.empty((0, K), dtype=torch.bfloat16, device=cuda)).shape == (0, 136)
+    proj = cr.ConvRotLinear.from_dense(torch.ones((8, K), device=cuda), group=64)
+    proj.set_lora_bank(torch.ones((E, 16, K), device=cuda), torch.ones((E, 8, 16), device=cuda),
+                       torch.ones(E, device=cuda))
+    plan = cr.group_rows(torch.empty(0, dtype=torch.int32, device=cuda), E)
+    assert proj(torch.empty((0, K), dtype=torch.bfloat16, device=cuda), groups=plan).shape == (0, 8)
+    assert torch.equal(plan.offsets, torch.zeros_like(plan.offsets))
+
+
 def test_experts_and_adapters_replay_in_a_graph(cuda):
     """One captured graph of a whole step (experts, then a projection with
     adapters per row), replayed with new inputs and new ids in place and
