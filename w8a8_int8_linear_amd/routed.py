@@ -173,7 +173,11 @@ def group_rows(ids: torch.Tensor, groups: int, out: RowGroups | None = None) -> 
     pairs, dev = ids.numel(), ids.device
     if out is None:
         sizes = [pairs, groups + 1, row_groups_tiles(pairs, groups)]
-        out = RowGroups(*torch.empty((sum(sizes),), dtype=torch.int32, device=dev).split(sizes), groups, per_row)
+        buf = torch.empty((sum(sizes),), dtype=torch.int32, device=dev)
+        out = RowGroups(*buf.split(sizes), groups, per_row)
+        at = buf.data_ptr()  # (what _check would find)
+        object.__setattr__(out, "_checked", _lib.RowGroups(at, at + 4 * sizes[0], at + 4 * (sizes[0] + sizes[1]), pairs,
+                                                           groups, per_row))
     elif (out.pairs, out.groups, out.per_row) != (pairs, groups, per_row):
         raise ValueError("out is a plan of other sizes")
     _need_device(out.order, dev, "out")
