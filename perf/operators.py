@@ -274,7 +274,7 @@ def _run_plain(s):
         return (y * s["weights"][..., None]).sum(1).to(s["y"].dtype)
     order, counts = s["order"], s["counts"]
     if op == "lora":
-        out = s["y"].to(torch.float32, copy=True)  # (y itself stays: the state is run again)
+        out = s["y"].float()
         for e, p0, p1 in _spans(counts, E):
             rows = order[p0:p1]
             t = s["x"][rows].float() @ s["a"][e].float().T
