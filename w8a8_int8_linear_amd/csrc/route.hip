@@ -314,6 +314,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
     return ra.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - mx) * inv_sum;
   };
   auto error = [&](float s, float c) { return kU * ((ra.sigmoid ? 2.1f : 36.f * s + 1.f) + fabsf(c)); };
+  // The row's largest score.  Comparisons take the error it gives for every
+  // value: with each one's own, a gap between two small scores would count
+  // as settled although a value further down, of a large score, may truly lie
+  // above both.  With one bound (c's own rounding moves by less than c does)
+  // a gap between neighbours also separates all values above it from all below.
+  const float s_max = ra.sigmoid ? 1.f : inv_sum;
 
   bool doubt = false;  // a choice the fp32 values do not settle
   if constexpr (WIDE) {
@@ -355,7 +361,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
       int lanes_g = L;
       while (lanes_g > 1 && L / lanes_g < ra.groups) lanes_g >>= 1;
       float err = 0.f;  // of a group's value: two choice values and their sum
-      const float s_max = ra.sigmoid ? 1.f : inv_sum;
       for (int g0 = 0; g0 < ra.groups; g0 += L / lanes_g) {
         const int g = g0 + l / lanes_g;
         float a = low, b = low;  // a >= b
@@ -413,7 +418,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
 
   // The k largest, one at a time; lane t of the row keeps the t-th.  Where c
   // decides, two more are taken: neighbours must differ by more than their
-  // errors, or the first k + 1 are ordered again by their fp64 values.
+  // errors (of the row's largest score), or the first k + 1 are ordered again
+  // by their fp64 values.
   const bool check = WIDE && bias != nullptr;
   const int picks = ra.k + (check ? 2 : 0);
   int mine = -1;
@@ -435,7 +441,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
   float mine_x = mine >= 0 ? load_logit(row + mine) : 0.f;
   if (check) {
     const float c = mine >= 0 ? key_value(mine_key) : 0.f;
-    const float err = mine >= 0 ? error(score(mine_x), c) : 0.f;
+    const float err = error(s_max, c);
     const float c_next = __shfl(c, lane + 1), err_next = __shfl(err, lane + 1);
     const int next = __shfl(mine, lane + 1);
     // lane t: its choice and the next are not told apart
