@@ -52,3 +52,26 @@ def test_route_near_ties_of_scores_of_different_size(cuda, E, k):
             # equal up to choices whose fp64 values differ by less than their own rounding
             c = R.choice_values(x[m], "softmax", bias)
             assert np.allclose(c[ids[m]], c[ids_ref[m]], rtol=0, atol=4e-16), m
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_group_values_past_fp32(cuda, score):
+    """Biases whose sum over two experts of a group leaves fp32's range (the
+    lowest value as a mask, large ones): group values are compared as fp64
+    values, so such a group is neither lost nor tied with another."""
+    g = np.random.default_rng(5)
+    for M, E, groups in ((9, 16, 4), (5, 96, 24), (3, 600, 8)):
+        per = E // groups
+        x = g.standard_normal((M, E)).astype(np.float32)
+        for value in (LOW, -3e38, 3e38):
+            for top, k in ((groups, 12), (groups // 2 + 1, 5), (1, 2)):
+                bias = (0.1 * g.standard_normal(E)).astype(np.float32)
+                far = g.permutation(groups)[:groups // 2 + 1]      # whole groups, in steps of their own
+                for i, f in enumerate(far):
+                    bias[f * per:(f + 1) * per] = np.float32(value) * np.float32(1 - 0.02 * i)
+                bias[far[0] * per] = 0.5                           # one of them has an ordinary expert left
+                for renorm in (True, False):
+                    ids, w = _route(x, k, score=score, bias=bias, groups=groups, top_groups=top, renormalise=renorm)
+                    ids_ref, w_ref = R.route(x, k, score, bias, groups, top, renorm)
+                    assert np.array_equal(ids, ids_ref), (E, value, top)
+                    assert np.all(np.abs(w - w_ref) <= (64 + E + 16) * R.U * np.abs(w_ref)), (E, value, top)

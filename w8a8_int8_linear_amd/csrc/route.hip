@@ -361,6 +361,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
       int lanes_g = L;
       while (lanes_g > 1 && L / lanes_g < ra.groups) lanes_g >>= 1;
       float err = 0.f;  // of a group's value: two choice values and their sum
+      bool past = false;  // a value that fp32 does not hold (biases next to its largest number)
       for (int g0 = 0; g0 < ra.groups; g0 += L / lanes_g) {
         const int g = g0 + l / lanes_g;
         float a = low, b = low;  // a >= b
@@ -379,8 +380,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
         }
         if (g < ra.groups && l % lanes_g == 0) {
           gv[g] = b > low ? a + b : a;
-          if (a > low)
+          if (a > low) {
             err = fmaxf(err, 2.f * error(s_max, a) + kU * (b > low ? fabsf(b) + fabsf(a + b) : 0.f));
+            past = past || fabsf(gv[g]) > 3.402823466e38f;
+          }
         }
       }
       wave_sync();
@@ -404,7 +407,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
       worst = -row_reduce<L>(-worst, max_f);
       best_out = row_reduce<L>(best_out, max_f);
       err = row_reduce<L>(err, max_f);
-      doubt = best_out > low && worst - best_out <= 2.f * err;
+      doubt = past || (best_out > low && worst - best_out <= 2.f * err);
       // the expert's group, i / per_group, by a product (half a group's width
       // away from the next integer, exact for these sizes)
       const float inv_group = 1.f / static_cast<float>(per_group);
