@@ -587,9 +587,13 @@ typedef struct {
  * closes an expert: it counts nowhere and is not chosen.  A bias of -inf or
  * NaN only keeps its expert from being chosen and from its group's value.  A
  * group without such an expert left is not kept.  Where fewer than k
- * experts are left, the remaining ids are -1 and their weights 0; a sum of
- * zero leaves zero weights.  A logit of +inf counts as the largest finite
- * value.
+ * experts are left, the remaining ids are -1 and their weights 0.  A logit
+ * of +inf counts as the largest finite fp32 value.  A score that fp64 does
+ * not hold is zero (1 / (1 + e^{-l}): l below -709; softmax: 745 below the
+ * largest logit), and a sum of zero leaves zero weights; the ratios of other
+ * scores are kept in renormalised weights, also where fp32 does not hold the
+ * scores.  A weight (not renormalised: a score) below the smallest normal
+ * fp32 number may lose bits or be 0.
  * Without a bias experts are compared by their logits, exactly (the score is
  * monotone in the logit).  Choice values with a bias, and group values, are
  * compared as fp64 values.

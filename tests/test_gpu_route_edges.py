@@ -75,3 +75,71 @@ def test_route_group_values_past_fp32(cuda, score):
                     ids_ref, w_ref = R.route(x, k, score, bias, groups, top, renorm)
                     assert np.array_equal(ids, ids_ref), (E, value, top)
                     assert np.all(np.abs(w - w_ref) <= (64 + E + 16) * R.U * np.abs(w_ref)), (E, value, top)
+
+
+def _weights(x, ids, score):
+    """Renormalised weights of the chosen ids from the logarithms of their
+    scores (up to a constant per row): l - log(1 + e^l), or l.  Scores that
+    are zero in 64 bits stay zero."""
+    l = np.take_along_axis(x.astype(np.float64), np.maximum(ids, 0), 1)
+    zero = l < -709.7827 if score == "sigmoid" else l - x.max(1, keepdims=True).astype(np.float64) < -745.14
+    if score == "sigmoid":
+        l = np.where(l < 0, l - np.log1p(np.exp(np.minimum(l, 0))), -np.log1p(np.exp(-np.maximum(l, 0))))
+    e = np.where(zero, 0.0, np.exp(l - l.max(1, keepdims=True)))
+    return e / np.maximum(e.sum(1, keepdims=True), 1e-300)
+
+
+def _check_weights(x, ids, w, score, k, scale):
+    want = _weights(x, ids, score) * scale
+    # exponents of at most 200 that matter (below, the weight is nothing): off
+    # by a unit of themselves; exp, sums and quotients a few more.  Weights
+    # below the smallest normal number are off by that at most.
+    tol = (2 * 200 + 2 * k + 16) * R.U
+    assert np.all(np.abs(w - want) <= tol * want + 2.0 ** -126 * scale)
+    total = want.sum(1)
+    assert np.all(np.abs(w.astype(np.float64).sum(1) - total) <= (2 * k + 4) * R.U * scale)
+    assert (total > 0).any()
+
+
+@pytest.mark.parametrize("E,k", [(8, 3), (128, 8), (256, 20), (1000, 33)])
+def test_route_weights_of_scores_that_underflow(cuda, E, k):
+    """Renormalised weights depend on the ratios of the chosen scores, which
+    stay ordinary numbers where the scores do not: logistic scores of very
+    negative logits, and softmax scores far below the row's largest."""
+    g = np.random.default_rng(E)
+    M = 40
+    centre = g.choice([-2.0, -62.0, -87.0, -95.0, -104.0, -160.0, -800.0, -1e4, -1e30], (M, 1))
+    x = (centre + 6 * g.standard_normal((M, E))).astype(np.float32)
+    x[-1] = LOW
+    for bias in (None, (1e-3 * g.standard_normal(E)).astype(np.float32)):
+        for groups, top in ((1, 1), (2, 1) if E // 2 >= k else (2, 2)):
+            ids, w = _route(x, k, score="sigmoid", bias=bias, groups=groups, top_groups=top, scale=2.5)
+            ids_ref, _ = R.route(x, k, "sigmoid", bias, groups, top)
+            assert np.array_equal(ids, ids_ref)
+            _check_weights(x, ids, w, "sigmoid", k, 2.5)
+    # softmax: a bias keeps the experts of large score from being chosen
+    x = (centre + 6 * g.standard_normal((M, E))).astype(np.float32)
+    x[:, :E // 4] = 0.0
+    bias = (1e-3 * g.standard_normal(E)).astype(np.float32)
+    bias[:E // 4] = -np.inf
+    bias[0] = -3.0
+    kk = min(k, E - E // 4)
+    ids, w = _route(x, kk, bias=bias, scale=2.5)
+    assert np.array_equal(ids, R.route(x, kk, "softmax", bias)[0])
+    _check_weights(x, ids, w, "softmax", kk, 2.5)
+
+
+def test_route_weights_do_not_depend_on_the_path(cuda):
+    """Rows of equal scores, of which one in two also holds a near tie and is
+    decided in fp64, have equal weights."""
+    E, k = 64, 4
+    x = np.full((32, E), -140.0, dtype=np.float32)
+    x[:, :k] = np.float32([-95.0, -96.5, -97.0, -99.0])
+    bias = np.zeros(E, dtype=np.float32)
+    bias[:k] = [0.4, 0.3, 0.2, 0.1]
+    bias[k:] = -1.0
+    bias[40:50] = 0.1  # as the last of the four, and closed in every other row
+    x[::2, 40:50], x[1::2, 40:50] = -95.0, -np.inf
+    ids, w = _route(x, k, score="sigmoid", bias=bias)
+    assert np.array_equal(ids, np.tile(np.arange(k), (32, 1)))
+    _check_weights(x, ids, w, "sigmoid", k, 1.0)

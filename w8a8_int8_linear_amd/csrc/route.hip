@@ -100,6 +100,28 @@ __device__ __forceinline__ float load_logit(const T* p) {
 // A logit an expert can be chosen by (-inf and NaN mark experts that cannot).
 __device__ __forceinline__ bool open_logit(float x) { return x >= -3.402823466e38f; }
 
+// The score of logit x up to a factor common to a row's choices, most their
+// largest logit: renormalised weights depend on the ratios alone, and where
+// every chosen score underflows these still hold numbers (the largest's is 1, or
+// for logistic scores at least 1/2).
+//   e^x = e^most e^{x - most}
+//   1 / (1 + e^{-x}) = e^m / (e^m + e^{m - x}),  m = min(most, 0)
+// A score of zero in fp64 stays zero: e^{-x} past its largest number, or
+// e^{x - max} below half its smallest.
+template <typename T>
+__device__ __forceinline__ T ratio_score(bool sigmoid, float logit, float max_logit, float most_logit) {
+  if (sigmoid ? logit < -709.7827f : static_cast<double>(logit) - static_cast<double>(max_logit) < -745.1332191019412)
+    return T(0);
+  const T x = logit, most = most_logit;
+  auto e = [](T v) {
+    if constexpr (std::is_same_v<T, float>) return expf(v);
+    else return exp(v);
+  };
+  if (!sigmoid) return e(x - most);
+  const T m = most < T(0) ? most : T(0);
+  return T(1) / (e(m) + e(m - x));
+}
+
 // One row in fp64 with a whole wavefront: E / 64 (rounded up, NE) consecutive
 // experts per lane, so that among equal values the lowest lane holds the
 // lowest index.  choice: E doubles of LDS of the wavefront's own (groups > 1).
@@ -200,8 +222,11 @@ __device__ void route_row_exact(const L* row, int E, const float* bias, const Ro
         if (j == at) key[j] = 0;
     }
   }
-  double s = mine >= 0 ? score(load_logit(row + mine), mx, inv_sum) : 0.0;
+  const float mine_x = mine >= 0 ? load_logit(row + mine) : 0.f;
+  double s = mine >= 0 ? score(mine_x, mx, inv_sum) : 0.0;
   if (ra.renormalise) {
+    const uint32_t most = wave_max(mine >= 0 ? order_key(mine_x) : 0u);
+    if (mine >= 0) s = ratio_score<double>(ra.sigmoid, mine_x, mx, key_value(most));
     const double total = wave_sum(s);
     s = total > 0.0 ? s / total : 0.0;
   }
@@ -491,6 +516,15 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
   float s = 0.f;
   if (mine >= 0 && l < ra.k) s = score(mine_x);
   if (ra.renormalise) {
+    // e^-60 times 1 / E is an ordinary fp32 number; scores below that are
+    // taken relative to the row's largest choice
+    const bool chosen = mine >= 0 && l < ra.k;
+    const bool far = chosen && (ra.sigmoid ? mine_x : mine_x - mx) < -60.f;
+    if (__ballot(far) != 0) {  // (uniform)
+      const uint32_t most = row_reduce<L>(chosen ? order_key(mine_x) : 0u, max_u);
+      const bool row_far = ((__ballot(far) >> base) & kRowLanes) != 0;
+      if (chosen && row_far) s = ratio_score<float>(ra.sigmoid, mine_x, mx, key_value(most));
+    }
     const float total = row_reduce<L>(s, add_f);
     s = total > 0.f ? s / total : 0.f;
   }
