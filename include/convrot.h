@@ -693,7 +693,9 @@ convrot_status convrot_combine_rows(const void* Y, convrot_dtype dt, int64_t ldy
  *   out[m, n] = Y[m, n] + scales[g] * sum_j T[m, j] B_g[n, j]
  * and out[m] = Y[m] for a row without a group (not touched where out is Y).
  * T is not rounded to bf16: it enters the second product as the sum of two
- * bf16 terms (bf16 Y) or three (fp32 Y).
+ * bf16 terms (bf16 Y; off by 2^-16 of T at most) or three (fp32 Y; 2^-24).
+ * Infinities of T and B give the formula's infinity or NaN (an infinity of B
+ * times a |T| below 2^-94 may be a NaN).
  *   X        [M, ldx] bf16, unrotated; A [groups][r, lda] and
  *            B [groups][N, ldb] bf16, stacked stride_a and stride_b elements
  *            apart (at least r * lda, N * ldb); adapters of lower rank

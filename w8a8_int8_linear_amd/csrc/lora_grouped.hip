@@ -15,7 +15,7 @@
 //    It adds the K blocks' sums of its rows once and keeps them in registers
 //    as bf16 terms: two (hi + lo, 16 bits of the fp32 sum) for a bf16 output,
 //    three (24 bits, all of it) for an fp32 one, so that the correction is
-//    not rounded before the output is.  The sums are staged in LDS so that Y
+//    not rounded before the output is (split_terms).  The sums are staged in LDS so that Y
 //    is read and out written in whole 128-byte lines, and with 64-row tiles
 //    B's rows pass through LDS once for the four waves.  Bound by Y and out.
 //
@@ -49,6 +49,31 @@ constexpr int kSteps = RT <= 2 ? 2 : 1;
 __device__ __forceinline__ f32x4 mma_bf16(const i32x4& a, const i32x4& b, const f32x4& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);
+}
+
+// v as a sum of N bf16 terms of v's sign, none of them zero unless v is: an
+// infinity of B then gives N infinities of one sign, and the sum is the
+// formula's infinity (with a term of zero or of the other sign it would be a
+// NaN).  All terms but the last are rounded towards zero, which also keeps
+// what lies above bf16's largest number finite; the sum is off by at most 2^-16
+// (N = 2) or 2^-24 (N = 3) of v.  Where nothing is left, 2^-32 of the first
+// term stands in for zero (below |v| = 2^-94 it may be zero itself).  Every
+// term of an infinity or a NaN is v.
+template <int N>
+__device__ __forceinline__ void split_terms(float v, __bf16 (&term)[N]) {
+  float first = 0.f;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    if (q > 0 && v == 0.f) {
+      term[q] = static_cast<__bf16>(first * 2.3283064365386963e-10f);  // 2^-32
+      continue;
+    }
+    term[q] = q == N - 1 ? static_cast<__bf16>(v)
+                         : static_cast<__bf16>(__builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u));
+    const float t = static_cast<float>(term[q]);
+    if (q == 0) first = t;
+    v = fabsf(t) <= 3.402823466e38f ? v - t : 0.f;
+  }
 }
 
 struct LoraArgs {
@@ -326,13 +351,10 @@ __global__ __launch_bounds__(64 * kUpWaves) void lora_grouped_up_kernel(LoraArgs
         const f32x4 lo = from[0], hi = from[1];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float rest = e < 4 ? lo[e % 4] : hi[e % 4];
+          __bf16 term[kTerms];
+          split_terms(e < 4 ? lo[e % 4] : hi[e % 4], term);
 #pragma unroll
-          for (int q = 0; q < kTerms; ++q) {
-            t[s][q][e] = static_cast<__bf16>(rest);
-            const float term = static_cast<float>(t[s][q][e]);
-            rest = fabsf(term) <= 3.402823466e38f ? rest - term : 0.f;  // nothing follows an infinity or a NaN
-          }
+          for (int q = 0; q < kTerms; ++q) t[s][q][e] = term[q];
         }
       }
       wave_sync();
