@@ -1,0 +1,42 @@
+"""Plans as Python objects, and calls of the binding for rows that choose
+their weights that end before a launch."""
+
+import copy
+import pickle
+
+import pytest
+import torch
+
+import w8a8_int8_linear_amd as cr
+from w8a8_int8_linear_amd import _lib
+
+
+def _plan(pairs=32, groups=4, per_row=2):
+    n = cr.row_groups_tiles(pairs, groups)
+    return cr.RowGroups(torch.arange(pairs, dtype=torch.int32), torch.zeros(groups + 1, dtype=torch.int32),
+                        torch.zeros(n, dtype=torch.int32), groups, per_row)
+
+
+def test_a_used_plan_can_be_copied():
+    """A plan that has served a call holds the descriptor of its buffers; a
+    copy has buffers of its own and takes none of it along."""
+    p = _plan()
+    object.__setattr__(p, "_checked", _lib.RowGroups(1 << 20, 2 << 20, 3 << 20, 32, 4, 2))  # as after a call
+    for q in (copy.deepcopy(p), pickle.loads(pickle.dumps(p))):
+        assert torch.equal(q.order, p.order) and q.order.data_ptr() != p.order.data_ptr()
+        assert (q.pairs, q.groups, q.per_row) == (32, 4, 2)
+        assert "_checked" not in q.__dict__
+    assert "_checked" not in copy.copy(p).__dict__
+    assert p.descriptor().pairs == 32
+
+
+@pytest.mark.gpu
+def test_a_copied_plan_is_independent(cuda):
+    ids = torch.tensor([[0, 2], [1, 2], [2, 0]], dtype=torch.int32, device=cuda)
+    p = cr.group_rows(ids, 3)
+    q = copy.deepcopy(p)
+    want = q.order.clone()
+    cr.group_rows(ids.flip(0).contiguous(), 3, out=p)
+    assert torch.equal(q.order, want) and not torch.equal(p.order, want)
+    cr.group_rows(ids.flip(0).contiguous(), 3, out=q)
+    assert torch.equal(q.order, p.order) and torch.equal(q.offsets, p.offsets)

@@ -138,6 +138,10 @@ class RowGroups:
             object.__setattr__(self, "_checked", desc)
         return desc
 
+    def __getstate__(self) -> dict:
+        # a copy has buffers of its own: it is checked anew
+        return {k: v for k, v in self.__dict__.items() if k != "_checked"}
+
     def _check(self) -> _lib.RowGroups:
         for t, name in ((self.order, "order"), (self.offsets, "offsets"), (self.tiles, "tiles")):
             if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
