@@ -40,3 +40,25 @@ def test_a_copied_plan_is_independent(cuda):
     assert torch.equal(q.order, want) and not torch.equal(p.order, want)
     cr.group_rows(ids.flip(0).contiguous(), 3, out=q)
     assert torch.equal(q.order, p.order) and torch.equal(q.offsets, p.offsets)
+
+
+def _packed(rows, K=256):
+    return cr.Packed(torch.zeros((rows, K), dtype=torch.int8), torch.ones(rows), 256)
+
+
+def _packed_w4(rows, K=256):
+    return cr.PackedW4(torch.zeros((rows, K // 2), dtype=torch.uint8), torch.ones(rows), K, 256)
+
+
+@pytest.mark.parametrize("wrong", [_packed_w4(256), torch.zeros(256, 256, dtype=torch.int8)])
+def test_grouped_linears_take_int8_rows_only(wrong):
+    """A packed int4 weight or bare codes are refused by name, whichever
+    operand they are given as."""
+    x, w = _packed(16), _packed(256)
+    for call in (lambda: cr.linear_grouped(x, wrong, _plan()), lambda: cr.linear_grouped(wrong, w, _plan()),
+                 lambda: cr.linear_gated_grouped(x, wrong, w, _plan()),
+                 lambda: cr.linear_gated_grouped(x, w, wrong, _plan())):
+        with pytest.raises(ValueError, match="must be int8 rows"):
+            call()
+    with pytest.raises(ValueError, match="must be int8 rows"):
+        cr.ConvRotExperts(torch.zeros(4, 256), wrong, w, w, 2)

@@ -246,6 +246,8 @@ class ConvRotExperts:
                  score: str = routed.SOFTMAX, bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1,
                  renormalise: bool = True, scale: float = 1.0, act: str = routed.SILU):
         E, K = router.shape
+        for t, name in ((gate, "gate"), (up, "up"), (down, "down")):
+            routed.need_packed(t, name)
         if gate.rows != up.rows or gate.rows % E or down.rows % E or gate.K != K or up.K != K or \
                 down.K != gate.rows // E:
             raise ValueError("router [E, K], gate and up [E * I, K] and down [E * N, I] do not fit")

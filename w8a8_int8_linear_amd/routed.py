@@ -195,7 +195,16 @@ def group_rows(ids: torch.Tensor, groups: int, out: RowGroups | None = None) -> 
 # The experts' products
 # ---------------------------------------------------------------------------
 
+def need_packed(t, name: str) -> None:
+    """``t`` must be a packed int8 operand (there are no grouped linears over
+    int4 weights)."""
+    if not isinstance(t, Packed):
+        raise ValueError(f"{name} must be int8 rows (Packed), got {type(t).__name__}")
+
+
 def _grouped(act: Packed, w: Packed, groups: RowGroups, bias, source: str, dest: str, out, out_dtype, name="bias"):
+    need_packed(act, "the activation")
+    need_packed(w, "the weight")
     if source not in _ORDER:
         raise ValueError(f"source must be one of {sorted(_ORDER)}")
     if dest not in (BY_PAIR, SORTED):
@@ -248,6 +257,7 @@ def linear_gated_grouped(act_in: Packed, w_gate: Packed, w_up: Packed, groups: R
     (convrot_linear_gated_grouped); arguments as ``linear_grouped``."""
     if act is None or act not in _FN:
         raise ValueError(f"activation must be one of {sorted(k for k in _FN if k)}")
+    need_packed(w_up, "the up weight")
     out = _grouped(act_in, w_gate, groups, b_gate, source, dest, out, out_dtype, "b_gate")
     _check_bias(b_up, w_up.rows, act_in.q.device, "b_up")
     _need_device(w_up.q, act_in.q.device, "the up weight")
