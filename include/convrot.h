@@ -630,7 +630,8 @@ convrot_status convrot_row_groups_tiles(int64_t pairs, int64_t groups, int64_t* 
 /* Writes the plan of ids [pairs] (int32, dense) into out's buffers.  A stable
  * counting sort without atomics across workgroups: the same ids give the
  * same plan.  One launch up to 8192 pairs, two above.  A plan serves any
- * number of calls; a call that reads it must be ordered behind this one. */
+ * number of calls; a call that reads it must be ordered behind this one.  The
+ * ids and the three buffers must not overlap. */
 convrot_status convrot_group_rows(const int32_t* ids, const convrot_row_groups* out, void* stream);
 
 /* Which row of an operand belongs to position i of a plan's order, with

@@ -62,3 +62,38 @@ def test_grouped_linears_take_int8_rows_only(wrong):
             call()
     with pytest.raises(ValueError, match="must be int8 rows"):
         cr.ConvRotExperts(torch.zeros(4, 256), wrong, w, w, 2)
+
+
+A, B, C, D = 0x1000000, 0x2000000, 0x3000000, 0x4000000
+
+
+@pytest.mark.parametrize("ids,order,offsets,tiles", [
+    (A, A, B, C), (A + 4 * 19999, A, B, C), (A - 4 * 19999, A, B, C), (B, A, B, C), (B + 4 * 40, A, B, C),
+    (C + 4 * 9, A, B, C), (D, A, A + 4 * 7, C), (D, A, B, A), (D, A, C + 8, C)])
+def test_group_rows_refuses_buffers_that_overlap(ids, order, offsets, tiles):
+    """The ids are read while the plan is written: ids inside one of the
+    plan's buffers would change under the workgroups that place them."""
+    lib = _lib.load()
+    p = _lib.RowGroups(order, offsets, tiles, 20000, 40, 1)
+    assert lib.convrot_group_rows(ids, p, None) == _lib.ERR_INVALID_ARG
+    assert b"overlap" in lib.convrot_last_error()
+
+
+def test_group_rows_counts_whole_buffers():
+    """The buffers' ends: every byte of the tiles counts, the next does not."""
+    lib = _lib.load()
+    p = _lib.RowGroups(A, B, C, 20000, 40, 1)
+    n = cr.row_groups_tiles(20000, 40)
+    assert lib.convrot_group_rows(C + 4 * (n - 1), p, None) == _lib.ERR_INVALID_ARG
+    assert b"overlap" in lib.convrot_last_error()
+    p = _lib.RowGroups(A, B, A + 4 * 19999, 20000, 40, 1)
+    assert lib.convrot_group_rows(D, p, None) == _lib.ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_group_rows_of_a_plans_own_order(cuda):
+    p = cr.group_rows(torch.zeros(50, dtype=torch.int32, device=cuda), 3)
+    with pytest.raises(cr.ConvrotError, match="overlap"):
+        cr.group_rows(p.order, 3, out=p)
+    q = cr.group_rows(p.order, 3)  # into buffers of its own: ids 0, 1, 2 and others
+    assert q.offsets.tolist() == [0, 1, 2, 3]

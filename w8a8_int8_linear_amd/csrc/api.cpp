@@ -1062,6 +1062,22 @@ convrot_status convrot_group_rows(const int32_t* ids, const convrot_row_groups* 
   if (st != CONVROT_OK) return st;
   if (out->pairs > 0 && ids == nullptr) return fail(CONVROT_ERR_INVALID_ARG, "%s: ids is NULL", what);
   if ((reinterpret_cast<uintptr_t>(ids) & 3u) != 0) return fail(CONVROT_ERR_ALIGN, "%s: ids must be 4-byte aligned", what);
+  // The workgroups read the ids more than once while others write the plan.
+  const struct {
+    const int32_t* p;
+    int64_t n;
+  } buf[] = {{ids, out->pairs},
+             {out->order, out->pairs},
+             {out->offsets, out->groups + int64_t{1}},
+             {out->tiles, convrot::plan_ints(out->pairs, out->groups)}};
+  for (int i = 0; i < 4; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(buf[i].p), a_end = a + 4 * buf[i].n;
+    for (int j = 0; j < i; ++j) {
+      const uintptr_t b = reinterpret_cast<uintptr_t>(buf[j].p), b_end = b + 4 * buf[j].n;
+      if (buf[i].n > 0 && buf[j].n > 0 && a < b_end && b < a_end)
+        return fail(CONVROT_ERR_INVALID_ARG, "%s: ids and the row groups' buffers overlap", what);
+    }
+  }
   return from_hip(convrot::launch_group_rows(ids, out->pairs, out->groups, out->order, out->offsets, out->tiles,
                                              static_cast<hipStream_t>(stream)),
                   what);
