@@ -143,3 +143,18 @@ def test_route_weights_do_not_depend_on_the_path(cuda):
     ids, w = _route(x, k, score="sigmoid", bias=bias)
     assert np.array_equal(ids, np.tile(np.arange(k), (32, 1)))
     _check_weights(x, ids, w, "sigmoid", k, 1.0)
+
+
+@pytest.mark.parametrize("M,E,k,dt", [((1 << 28) + 37, 2, 1, torch.bfloat16), ((1 << 26) + 5, 34, 31, torch.bfloat16)])
+def test_route_more_rows_than_one_launch_holds(cuda, M, E, k, dt):
+    """A launch holds fewer than 2^32 threads: 2^28 rows of sixteen lanes, or
+    2^26 of sixty-four."""
+    x = torch.zeros((M, E), dtype=dt, device=cuda)
+    x[:, E - 1] = 1.0
+    x[0, 0], x[-1, 0], x[M // 2, 0] = 2.0, 2.0, 2.0
+    ids, w = cr.route(x, k, ids=torch.full((M, k), -7, dtype=torch.int32, device=cuda))
+    first = ids[:, 0]
+    assert int((first != E - 1).sum()) == 3
+    assert first[0] == 0 and first[-1] == 0 and first[M // 2] == 0
+    assert torch.equal(ids[1], ids[-2]) and torch.equal(ids[0], ids[-1])
+    assert torch.equal(w[1], w[-2]) and torch.equal(w[0], w[-1])

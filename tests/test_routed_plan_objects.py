@@ -97,3 +97,22 @@ def test_group_rows_of_a_plans_own_order(cuda):
         cr.group_rows(p.order, 3, out=p)
     q = cr.group_rows(p.order, 3)  # into buffers of its own: ids 0, 1, 2 and others
     assert q.offsets.tolist() == [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("gated,N", [(False, 500000), (True, 250000)])
+def test_grouped_launches_of_too_many_threads_are_refused(gated, N):
+    """A launch holds fewer than 2^32 threads; the weight-streaming form of
+    many narrow groups with very many features would need more."""
+    lib = _lib.load()
+    E, pairs = 4096, 20480
+    p = _lib.RowGroups(A, B, C, pairs, E, 1)
+    rot = _lib.Rot(16, _lib.ROT_REGULAR, None)
+    act = _lib.Packed(A, B, pairs, 16, 16, rot, _lib.LAYOUT_ROWS)
+    w = _lib.Packed(C, D, E * N, 16, 16, rot, _lib.LAYOUT_ROWS)
+    if gated:
+        st = lib.convrot_linear_gated_grouped(act, w, None, w, None, _lib.ACT_SILU, p, _lib.BY_ROW, _lib.SORTED, D,
+                                              _lib.BF16, N, None)
+    else:
+        st = lib.convrot_linear_grouped(act, w, None, _lib.ACT_NONE, p, _lib.BY_ROW, _lib.SORTED, D, _lib.BF16, N, None)
+    assert st == _lib.ERR_INVALID_ARG
+    assert b"threads" in lib.convrot_last_error()

@@ -949,6 +949,13 @@ convrot_status check_grid(const char* what, int64_t blocks) {
   return CONVROT_OK;
 }
 
+// The status of a launcher that may find its grid too large.
+convrot_status from_launch(hipError_t e, const char* what) {
+  if (e == hipErrorInvalidConfiguration)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: the problem needs more threads than one launch holds", what);
+  return from_hip(e, what);
+}
+
 // Whether two matrices of `cols` columns share memory (column slices of one
 // wider matrix do not).
 bool overlap(const void* p, int64_t rows_p, int64_t ldp, const void* q, int64_t rows_q, int64_t ldq, int64_t cols,
@@ -1093,12 +1100,12 @@ convrot_status convrot_linear_grouped(const convrot_packed* act, const convrot_p
   const convrot_status st = check_grouped(what, act, w, bias, groups, source, dest, Y, ydt, ldy);
   if (st != CONVROT_OK) return st;
   const convrot::RowPlan plan = row_plan(groups);
-  return from_hip(convrot::launch_linear_grouped(
-                      act->q, act->ld, w->q, w->ld, act->scale, w->scale, bias, nullptr, 0, nullptr, nullptr, false,
-                      static_cast<convrot::Act>(fn), plan, static_cast<convrot::RowOrder>(source),
-                      static_cast<convrot::RowOrder>(dest), w->rows / groups->groups, act->K, Y,
-                      static_cast<convrot::Elt>(ydt), ldy, static_cast<hipStream_t>(stream)),
-                  what);
+  return from_launch(convrot::launch_linear_grouped(
+                         act->q, act->ld, w->q, w->ld, act->scale, w->scale, bias, nullptr, 0, nullptr, nullptr, false,
+                         static_cast<convrot::Act>(fn), plan, static_cast<convrot::RowOrder>(source),
+                         static_cast<convrot::RowOrder>(dest), w->rows / groups->groups, act->K, Y,
+                         static_cast<convrot::Elt>(ydt), ldy, static_cast<hipStream_t>(stream)),
+                     what);
 }
 
 convrot_status convrot_linear_gated_grouped(const convrot_packed* act, const convrot_packed* w_gate,
@@ -1117,13 +1124,13 @@ convrot_status convrot_linear_gated_grouped(const convrot_packed* act, const con
   st = check_grouped(what, act, w_up, b_up, groups, source, dest, Y, ydt, ldy);
   if (st != CONVROT_OK) return st;
   const convrot::RowPlan plan = row_plan(groups);
-  return from_hip(convrot::launch_linear_grouped(
-                      act->q, act->ld, w_gate->q, w_gate->ld, act->scale, w_gate->scale, b_gate, w_up->q, w_up->ld,
-                      w_up->scale, b_up, true, static_cast<convrot::Act>(fn), plan,
-                      static_cast<convrot::RowOrder>(source), static_cast<convrot::RowOrder>(dest),
-                      w_gate->rows / groups->groups, act->K, Y, static_cast<convrot::Elt>(ydt), ldy,
-                      static_cast<hipStream_t>(stream)),
-                  what);
+  return from_launch(convrot::launch_linear_grouped(
+                         act->q, act->ld, w_gate->q, w_gate->ld, act->scale, w_gate->scale, b_gate, w_up->q, w_up->ld,
+                         w_up->scale, b_up, true, static_cast<convrot::Act>(fn), plan,
+                         static_cast<convrot::RowOrder>(source), static_cast<convrot::RowOrder>(dest),
+                         w_gate->rows / groups->groups, act->K, Y, static_cast<convrot::Elt>(ydt), ldy,
+                         static_cast<hipStream_t>(stream)),
+                     what);
 }
 
 convrot_status convrot_combine_rows(const void* Y, convrot_dtype dt, int64_t ldy, const float* weights,
@@ -1217,10 +1224,10 @@ convrot_status convrot_lora_add_grouped(const void* X, int64_t ldx, int64_t M, i
   // the second product's grid, the larger of the two
   st = check_grid(what, convrot::plan_max_tiles(M, groups->groups, 0) * std::max<int64_t>((N + 63) / 64, 32));
   if (st != CONVROT_OK) return st;
-  return from_hip(convrot::launch_lora_grouped(X, ldx, A, lda, stride_a, B, ldb, stride_b, scales, M, K, N, r,
-                                               row_plan(groups), Y, ldy, out, ldo, static_cast<convrot::Elt>(dt),
-                                               workspace, static_cast<hipStream_t>(stream)),
-                  what);
+  return from_launch(convrot::launch_lora_grouped(X, ldx, A, lda, stride_a, B, ldb, stride_b, scales, M, K, N, r,
+                                                  row_plan(groups), Y, ldy, out, ldo, static_cast<convrot::Elt>(dt),
+                                                  workspace, static_cast<hipStream_t>(stream)),
+                     what);
 }
 
 const char* convrot_status_string(convrot_status status) {

@@ -22,16 +22,17 @@ template <int OUT, bool GATED, bool KTAIL, int MT, int NW, bool SPLIT>
 hipError_t launch_ring_typed(GroupedArgs a, const RowPlan& plan, hipStream_t stream) {
   auto kern = ring::grouped_ring_kernel<OUT, GATED, KTAIL, MT, NW, SPLIT>;
   constexpr int kSmem = ring::smem_bytes<MT, NW, SPLIT>();
+  constexpr int b = MT == 1 ? 0 : MT == 2 ? 1 : 2;
+  constexpr int kFeat = (GATED ? 16 : 32) * (SPLIT ? 1 : NW);
+  a.tiles_n = (a.N + kFeat - 1) / kFeat;
+  const int64_t blocks = plan_max_tiles(plan.pairs, plan.groups, b) * a.tiles_n;
+  if (blocks > kMaxLaunchThreads / (64 * NW)) return hipErrorInvalidConfiguration;
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kern), kSmem, lds_set);
   if (e != hipSuccess) return e;
-  constexpr int b = MT == 1 ? 0 : MT == 2 ? 1 : 2;
   a.list = plan.tiles + plan_list_at(plan.pairs, plan.groups, b);
   a.count = plan.tiles + b;
-  constexpr int kFeat = (GATED ? 16 : 32) * (SPLIT ? 1 : NW);
-  a.tiles_n = (a.N + kFeat - 1) / kFeat;
-  const dim3 grid(static_cast<unsigned>(plan_max_tiles(plan.pairs, plan.groups, b) * a.tiles_n));
-  hipLaunchKernelGGL(kern, grid, dim3(64 * NW), kSmem, stream, a);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(64 * NW), kSmem, stream, a);
   return hipGetLastError();
 }
 

@@ -226,6 +226,11 @@ hipError_t launch_combine_rows(const void* Y, Elt dt, int64_t ldy, const float* 
                                int64_t M, int64_t k, int64_t N, int64_t E, void* out, int64_t ldo,
                                hipStream_t stream);
 
+// Threads of a launch in one dimension: fewer than 2^32 (the runtime drops what
+// is above without an error).  Launchers split their rows, or return
+// hipErrorInvalidConfiguration before they launch anything.
+constexpr int64_t kMaxLaunchThreads = (int64_t{1} << 32) - 1;
+
 // A plan as the products read it: pair p of row p / per_row sits at position
 // i with order[i] = p.
 struct RowPlan {

@@ -495,12 +495,10 @@ hipError_t launch_down(const LoraArgs& a, int list, dim3 grid, hipStream_t strea
   return hipGetLastError();
 }
 
-template <int OUT, int KS>
-void launch_up(LoraArgs a, const RowPlan& plan, hipStream_t stream) {
+// Sets the second product's steps per wave and blocks of columns; its workgroups.
+int64_t up_blocks(LoraArgs& a) {
   const int b = tile_list(a.M, a.groups);
-  a.list = plan.tiles + plan_list_at(plan.pairs, plan.groups, b);
-  a.count = plan.tiles + kPlanLists + b;  // with the tiles of rows without an adapter
-  const int64_t tiles = plan_max_tiles(plan.pairs, plan.groups, b);
+  const int64_t tiles = plan_max_tiles(a.M, a.groups, b);
   const int ranges = b == 2 ? 1 : kUpWaves;  // column ranges per workgroup
   const int64_t steps = (a.N + 63) / 64;
   // Up to four steps per wave (a row's sums are read once for all of them)
@@ -509,7 +507,15 @@ void launch_up(LoraArgs a, const RowPlan& plan, hipStream_t stream) {
   while (per > 1 && tiles * ((steps + per * ranges - 1) / (per * ranges)) < 4 * device_cus()) per /= 2;
   a.col_steps = static_cast<int>(per);
   a.col_blocks = static_cast<int>((steps + per * ranges - 1) / (per * ranges));
-  const dim3 grid(static_cast<unsigned>(tiles * a.col_blocks));
+  return tiles * a.col_blocks;
+}
+
+template <int OUT, int KS>
+void launch_up(LoraArgs a, const RowPlan& plan, hipStream_t stream) {
+  const int b = tile_list(a.M, a.groups);
+  a.list = plan.tiles + plan_list_at(plan.pairs, plan.groups, b);
+  a.count = plan.tiles + kPlanLists + b;  // with the tiles of rows without an adapter
+  const dim3 grid(static_cast<unsigned>(up_blocks(a)));
   if (b == 2)
     hipLaunchKernelGGL((lora_grouped_up_kernel<OUT, KS, 4>), grid, dim3(64 * kUpWaves), 0, stream, a);
   else
@@ -573,7 +579,10 @@ hipError_t launch_lora_grouped(const void* X, int64_t ldx, const void* A, int64_
   a.nb = down_blocks(M, K, r, plan.groups);
   a.spb = static_cast<int>((down_steps(M, K, plan.groups) + a.nb - 1) / a.nb);
   a.rb = (a.r + kDownCols - 1) / kDownCols;
-  const dim3 grid(static_cast<unsigned>(plan_max_tiles(plan.pairs, plan.groups, b) * a.nb * a.rb));
+  const int64_t down = plan_max_tiles(plan.pairs, plan.groups, b) * a.nb * a.rb;
+  if (down > kMaxLaunchThreads / (64 * kDownWaves) || up_blocks(a) > kMaxLaunchThreads / (64 * kUpWaves))
+    return hipErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(down));
   const hipError_t e = r <= 16   ? launch_down<1>(a, b, grid, stream)
                        : r <= 32 ? launch_down<2>(a, b, grid, stream)
                        : r <= 64 ? launch_down<4>(a, b, grid, stream)

@@ -561,9 +561,14 @@ hipError_t launch_route_typed(const Lg* logits, int64_t ldl, int64_t M, int64_t 
   // fp32 choice and group values of the wavefront's rows, or one row in fp64
   ra.lds_doubles = ra.groups > 1 ? static_cast<int>(std::max<int64_t>(E, (64 / L * (L * NE + 64) + 1) / 2)) : 0;
   const size_t lds = sizeof(double) * kRouteWaves * ra.lds_doubles;  // at most 32 KiB
-  hipLaunchKernelGGL((route_kernel<Lg, L, NE, WIDE, NX>), dim3(static_cast<unsigned>((M + rows - 1) / rows)),
-                     dim3(64 * kRouteWaves), lds, stream, logits, ldl, static_cast<int>(M), static_cast<int>(E), bias,
-                     ra, ids, weights);
+  // (a launch holds 2^32 / 256 workgroups less one; more rows take several)
+  constexpr int64_t step = kMaxLaunchThreads / (64 * kRouteWaves) * rows;
+  for (int64_t m0 = 0; m0 < M; m0 += step) {
+    const int64_t m = std::min(step, M - m0);
+    hipLaunchKernelGGL((route_kernel<Lg, L, NE, WIDE, NX>), dim3(static_cast<unsigned>((m + rows - 1) / rows)),
+                       dim3(64 * kRouteWaves), lds, stream, logits + m0 * ldl, ldl, static_cast<int>(m),
+                       static_cast<int>(E), bias, ra, ids + m0 * ra.k, weights + m0 * ra.k);
+  }
   return hipGetLastError();
 }
 
