@@ -61,18 +61,16 @@ __device__ __forceinline__ f32x4 mma_bf16(const i32x4& a, const i32x4& b, const 
 // term of an infinity or a NaN is v.
 template <int N>
 __device__ __forceinline__ void split_terms(float v, __bf16 (&term)[N]) {
-  float first = 0.f;
+  auto cut = [](float x) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x) & 0xFFFF0000u); };
+  float t = cut(v);
+  const float small = t * 2.3283064365386963e-10f;  // 2^-32
+  term[0] = static_cast<__bf16>(t);
 #pragma unroll
-  for (int q = 0; q < N; ++q) {
-    if (q > 0 && v == 0.f) {
-      term[q] = static_cast<__bf16>(first * 2.3283064365386963e-10f);  // 2^-32
-      continue;
-    }
-    term[q] = q == N - 1 ? static_cast<__bf16>(v)
-                         : static_cast<__bf16>(__builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u));
-    const float t = static_cast<float>(term[q]);
-    if (q == 0) first = t;
-    v = fabsf(t) <= 3.402823466e38f ? v - t : 0.f;
+  for (int q = 1; q < N; ++q) {
+    v -= t;
+    v = fabsf(v) > 0.f ? v : small;  // (inf - inf: small is the infinity)
+    t = q < N - 1 ? cut(v) : v;
+    term[q] = static_cast<__bf16>(t);
   }
 }
 

@@ -517,10 +517,11 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const Lg* __res
   if (mine >= 0 && l < ra.k) s = score(mine_x);
   if (ra.renormalise) {
     // e^-60 times 1 / E is an ordinary fp32 number; scores below that are
-    // taken relative to the row's largest choice
+    // taken relative to the row's largest choice (for softmax without a bias
+    // or groups that is the largest logit, which they are relative to already)
     const bool chosen = mine >= 0 && l < ra.k;
     const bool far = chosen && (ra.sigmoid ? mine_x : mine_x - mx) < -60.f;
-    if (__ballot(far) != 0) {  // (uniform)
+    if ((WIDE || ra.sigmoid) && __ballot(far) != 0) {  // (uniform)
       const uint32_t most = row_reduce<L>(chosen ? order_key(mine_x) : 0u, max_u);
       const bool row_far = ((__ballot(far) >> base) & kRowLanes) != 0;
       if (chosen && row_far) s = ratio_score<float>(ra.sigmoid, mine_x, mx, key_value(most));
