@@ -247,7 +247,7 @@ enum class RowOrder : int { Row = 0, Pair = 1, Sorted = 2 };
 // Grouped linears over stacked weights [groups * N, K]: the rows of group e
 // meet weight rows e N .. (e + 1) N - 1.
 //   plain  Y = act(A sa sb + bias)            (act None; Gelu; Silu)
-//   gated  Y = act(A sa sb + bias) * (A sa sb2 + bias2)  with epi.B2
+//   gated  Y = act(A sa sb + bias) * (A sa sb2 + bias2), the second product with B2
 hipError_t launch_linear_grouped(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const float* sa,
                                  const float* sb, const float* bias, const int8_t* B2, int64_t ldb2, const float* sb2,
                                  const float* bias2, bool gated, Act act, const RowPlan& plan, RowOrder source,

@@ -7,7 +7,8 @@
 // choice values c_i = s_i + b_i, the values of groups of experts (the sum of
 // the two largest c), and the k largest c among the groups kept, ties to the
 // lowest index.  Values are compared as unsigned keys whose order is that of
-// the numbers; key 0 is an expert that cannot be chosen.
+// the numbers; key 0 is an expert that cannot be chosen.  Renormalised weights
+// are fp32 too (a few units of 2^-24 off).
 //   Without a bias the score is a monotone function of the logit, and experts
 // are compared by their fp32 logits, exactly.  A bias and group values need c
 // itself, and two of them may differ by less than fp32 resolves: they are
@@ -18,9 +19,10 @@
 // fp32 logits are 8 MB, 1.5 us): 16 lanes take a row where its k allows (four
 // rows per wavefront), so that a maximum costs four lane exchanges for four
 // rows.  For those rows (k = 8, logistic, 8 groups, bias) fp64 throughout with
-// a wavefront per row took 23 us; this takes 11-13 us, and 15 us in launches
-// where some row has to be done again.  Without bias and groups: 7 us; one
-// row of 128: 3.9 us.
+// a wavefront per row took 23 us; this takes 11-13 us, and 15-16 us in launches
+// where some row has to be done again.  In a graph, launch included: with a
+// bias alone 12 (softmax) and 13 us (logistic), without bias and groups 7.6 us,
+// one row of 128 4.6 us (4.0 on its own).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -881,9 +883,11 @@ hipError_t launch_route(const void* logits, Elt dt, int64_t ldl, int64_t M, int6
               : launch_route_lanes<__bf16, false>(l, ldl, M, E, bias, ra, ids, weights, stream);
 }
 
-// Pairs counted by every workgroup anew, and pairs per chunk.  A chunk's
-// turns are serial, and every workgroup reads all chunks' counts: 1024 pairs
-// (16 turns) where the counts are added, 256 where each workgroup counts.
+// Pairs counted by every workgroup anew, and pairs per chunk.  Where the counts
+// are added, every workgroup reads those of all chunks, so a chunk is 1024
+// pairs: one pass of a workgroup's threads (beyond 1023 groups its sixteen
+// wavefronts take turns).  Where every workgroup counts all pairs anyway, 256,
+// so that more workgroups share the placing and the tile lists.
 static constexpr int64_t kPlanRecount = 8192;
 // 256 threads where the pairs and the groups are few (barriers and the scan over
 // wavefronts are what costs), 1024 otherwise (us, 256 and 1024 threads): 8 pairs

@@ -240,7 +240,13 @@ class ConvRotExperts:
     int8 path: bf16 router, choice of experts, grouped gate/up products,
     pack, grouped down product, weighted sum.  The packed weights are stacked
     over the experts; both widths must be multiples of the group size (there
-    is no bf16 path for experts)."""
+    is no bf16 path for experts).
+
+    Roundings to bf16, whatever the input's and the output's type: the
+    router's weights and its input (the framework's unpacked linear takes
+    bf16; its sums and the logits are fp32), and the inner activation
+    between the two products (the pack that follows keeps 8 bits of a row's
+    largest value, so a bf16 half step is small beside its own)."""
 
     def __init__(self, router: torch.Tensor, gate: api.Packed, up: api.Packed, down: api.Packed, top_k: int,
                  score: str = routed.SOFTMAX, bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1,
