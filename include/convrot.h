@@ -649,7 +649,9 @@ typedef enum {
  *           source CONVROT_BY_ROW, else pairs rows
  *   w       packed weights stacked over the groups, [groups * N, K], ROWS
  *           layout; same K and rotation as `act` (CONVROT_ERR_MISMATCH
- *           otherwise)
+ *           otherwise).  N is at most 2^31 - 1024, and a launch of 2^32
+ *           threads or more (many narrow groups with very many features) is
+ *           CONVROT_ERR_INVALID_ARG
  *   bias    [groups * N] fp32 or NULL
  *   fn      CONVROT_ACT_NONE, _GELU_ERF, _GELU_TANH or _SILU
  *   groups  a plan
@@ -703,7 +705,7 @@ convrot_status convrot_combine_rows(const void* Y, convrot_dtype dt, int64_t ldy
  *            are padded with zeros in both
  *   scales   [groups] fp32, on the device
  *   r        a positive multiple of 16, at most 256; K a positive multiple
- *            of 16
+ *            of 16; N at most 2^31 - 1024 (and fewer than 2^32 threads)
  *   groups   a plan with per_row 1 and M pairs
  *   Y, out   [M, ldy], [M, ldo] of dt, CONVROT_F32 or CONVROT_BF16; out is Y
  *            (with ldo == ldy) or does not overlap it

@@ -116,3 +116,24 @@ def test_grouped_launches_of_too_many_threads_are_refused(gated, N):
         st = lib.convrot_linear_grouped(act, w, None, _lib.ACT_NONE, p, _lib.BY_ROW, _lib.SORTED, D, _lib.BF16, N, None)
     assert st == _lib.ERR_INVALID_ARG
     assert b"threads" in lib.convrot_last_error()
+
+
+@pytest.mark.parametrize("what", ["plain", "gated", "lora"])
+def test_widths_next_to_2_31_are_refused(what):
+    """Kernels count features in 32 bits, whole blocks past the last one."""
+    lib = _lib.load()
+    N, wide = (1 << 31) - 1, 1 << 31
+    p = _lib.RowGroups(A, B, C, 1, 1, 1)
+    rot = _lib.Rot(16, _lib.ROT_REGULAR, None)
+    act = _lib.Packed(A, B, 1, 16, 16, rot, _lib.LAYOUT_ROWS)
+    w = _lib.Packed(C, D, N, 16, 16, rot, _lib.LAYOUT_ROWS)
+    if what == "plain":
+        st = lib.convrot_linear_grouped(act, w, None, _lib.ACT_NONE, p, _lib.BY_ROW, _lib.SORTED, D, _lib.BF16, wide, None)
+    elif what == "gated":
+        st = lib.convrot_linear_gated_grouped(act, w, None, w, None, _lib.ACT_SILU, p, _lib.BY_ROW, _lib.SORTED, D,
+                                              _lib.BF16, wide, None)
+    else:
+        st = lib.convrot_lora_add_grouped(A, 16, 1, 16, B, 16, 256, C, 16, wide * 16, N, 16, D, p, D, wide, _lib.BF16, D,
+                                          wide, A, 1 << 20, None)
+    assert st == _lib.ERR_INVALID_ARG
+    assert b"features" in lib.convrot_last_error()

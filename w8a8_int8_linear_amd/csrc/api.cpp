@@ -949,6 +949,15 @@ convrot_status check_grid(const char* what, int64_t blocks) {
   return CONVROT_OK;
 }
 
+// Kernels count features in 32 bits and in whole blocks of up to 1024.
+convrot_status check_width(const char* what, int64_t N) {
+  constexpr int64_t most = (int64_t{1} << 31) - 1024;
+  if (N < 0 || N > most)
+    return fail(CONVROT_ERR_INVALID_ARG, "%s: N = %lld features must be 0 to %lld", what, static_cast<long long>(N),
+                static_cast<long long>(most));
+  return CONVROT_OK;
+}
+
 // The status of a launcher that may find its grid too large.
 convrot_status from_launch(hipError_t e, const char* what) {
   if (e == hipErrorInvalidConfiguration)
@@ -1007,7 +1016,9 @@ convrot_status check_grouped(const char* what, const convrot_packed* act, const 
   const int64_t N = w->rows / g->groups;
   st = check_matrix("Y", Y, N > 0 ? g->pairs : 0, N, ldy, elt_size(ydt), false);
   if (st != CONVROT_OK) return st;
-  return check_grid(what, convrot::plan_max_tiles(g->pairs, g->groups, 0) * ((N + 15) / 16));
+  st = check_grid(what, convrot::plan_max_tiles(g->pairs, g->groups, 0) * ((N + 15) / 16));
+  if (st != CONVROT_OK) return st;
+  return check_width(what, N);
 }
 }  // namespace
 
@@ -1190,7 +1201,8 @@ convrot_status convrot_lora_add_grouped(const void* X, int64_t ldx, int64_t M, i
   if (groups->per_row != 1 || groups->pairs != M)
     return fail(CONVROT_ERR_MISMATCH, "%s: the row groups must hold one pair per row (per_row 1, %lld pairs)", what,
                 static_cast<long long>(M));
-  if (N < 0 || N > kMaxRows) return fail(CONVROT_ERR_INVALID_ARG, "%s: bad N", what);
+  st = check_width(what, N);
+  if (st != CONVROT_OK) return st;
   if (dt != CONVROT_F32 && dt != CONVROT_BF16)
     return fail(CONVROT_ERR_DTYPE, "%s: Y and out must be CONVROT_F32 or CONVROT_BF16", what);
   st = check_matrix("X", X, M, K, ldx, 2);
